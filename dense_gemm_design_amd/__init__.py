@@ -1,7 +1,9 @@
 """MI355X-native tiled dense GEMM (BF16, FP8 e4m3 with per-tensor FP32 scales, FP32 accumulate).
 
 The compute path is the HIP library libdgemm.so (csrc/, C ABI in include/gemm.h); this package
-is its Python binding.  See gemm() for a one-call helper on torch tensors.
+is its Python binding.  See gemm() for a one-call helper on torch tensors, and ops.py for the
+operators around the product: block-scaled e4m3 operands (block_quantize, BlockScaled, block_gemm),
+layer norm and its gradients, and gradient clipping.
 """
 from . import _lib
 from ._lib import (GemmDesc, GemmError, Plan, make_desc, load,  # noqa: F401
@@ -14,6 +16,8 @@ from ._lib import (GemmDesc, GemmError, Plan, make_desc, load,  # noqa: F401
                    GEMM_EPI_BIAS_ROW, GEMM_EPI_BIAS_COL, GEMM_EPI_RELU, GEMM_EPI_GELU,
                    GEMM_EPI_SILU, GEMM_EPI_AMAX, GEMM_EPI_SOURCE_F32, GEMM_EPI_SOURCE_BF16,
                    GemmEpilogueArgs)
+from .ops import (BlockScaled, block_gemm, block_quantize, clip_grad_norm,  # noqa: F401
+                  grad_norm, layer_norm, layer_norm_backward)
 
 KERNEL_NAMES = {0: "cooperative", 1: "ping-pong", 3: "wide-wave"}  # gemm_plan_info.kernel
 MAPPINGS = {"linear_n": GEMM_MAP_LINEAR_N, "linear_m": GEMM_MAP_LINEAR_M,

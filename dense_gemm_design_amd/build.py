@@ -1,8 +1,8 @@
 """Builds the HIP library libdgemm.so in-tree for gfx950 with hipcc.
 
 Each translation unit compiles to an object of its own, all at once (the wide-wave kernels that
-read a source matrix sit in gemm_src_*.hip for this), and the objects are linked into the
-shared library."""
+read a source matrix sit in gemm_src_*.hip for this; the operators around the product in
+ops_*.hip), and the objects are linked into the shared library."""
 import os
 import subprocess
 import sys
@@ -13,7 +13,8 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libdgemm.so")
 SOURCES = [os.path.join(CSRC, name)
-           for name in ("gemm.hip", "gemm_src_bf16.hip", "gemm_src_fp8.hip")]
+           for name in ("gemm.hip", "gemm_src_bf16.hip", "gemm_src_fp8.hip", "ops_block.hip",
+                        "ops_quantize.hip", "ops_norm.hip", "ops_clip.hip")]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 

@@ -1,0 +1,104 @@
+/*
+ * dense_gemm_design_amd -- C ABI of the operators around the product, for MI355X (gfx950):
+ *
+ *   gemm_block_quantize       e4m3 codes with one fp32 scale per block of 128
+ *   gemm_block_run            C = A B^T of two such operands, with a bias or a source matrix
+ *   gemm_layer_norm           layer norm, and
+ *   gemm_layer_norm_backward  its gradients
+ *   gemm_grad_norm            the norm of a list of gradients, and
+ *   gemm_clip_grad_norm       the list scaled to a largest norm
+ *
+ * Conventions are those of gemm.h: every function returns a gemm_status, checks its arguments
+ * before anything is enqueued, and enqueues kernels (nothing else) on `stream`; pointers are
+ * DEVICE pointers owned by the caller, and the library allocates no device memory.  Workspaces
+ * are sized by the functions beside each operator; their contents need no preparation and may be
+ * given to another call as soon as this one's work on the stream is done.  Element types are
+ * gemm_dtype values.  Results do not change from run to run.
+ */
+#ifndef DENSE_GEMM_DESIGN_AMD_GEMM_OPS_H
+#define DENSE_GEMM_DESIGN_AMD_GEMM_OPS_H
+
+#include "gemm.h"
+
+#ifdef __cplusplus
+extern "C" {
+#endif
+
+/* Blocks of one scale: 128 elements of a row, or 128 rows x 128 columns.  Blocks start at
+ * multiples of 128; the last ones of a matrix may be smaller. */
+typedef enum { GEMM_BLOCK_ROW = 0, GEMM_BLOCK_TILE = 1 } gemm_block;
+
+/* Block quantisation of x, rows x cols (GEMM_BF16 or GEMM_F32; element (i, j) at i * stride + j):
+ *   s = max(amax / 448, 2^-126) of each block (pow2: the smallest power of two that is not below
+ *   it; NaN where the block holds an infinity or a NaN), code = e4m3(x / s), the exact quotient
+ *   rounded to nearest even.
+ * codes: rows x pitch bytes, pitch = cols rounded up to 16, zeros behind each row's codes.
+ * scales: of block column j, row (or 128-row block) i at j * scale_pitch + i.
+ * codes_t, scales_t: the same of x transposed (cols x rows).  Either side may be NULL.
+ * codes and codes_t are 16-byte aligned. */
+int gemm_block_quantize(const void *x, int dtype, int64_t rows, int64_t cols, int64_t stride,
+                        int block, int pow2, void *codes, int64_t pitch, float *scales,
+                        int64_t scale_pitch, void *codes_t, int64_t pitch_t, float *scales_t,
+                        int64_t scale_pitch_t, void *stream);
+
+/* A product of block-scaled operands: C (M x N, packed rows) =
+ *   sum over k-blocks of scale_a[m, kb] scale_b[n or n / 128, kb] sum over k in kb of a b
+ *   + bias[n] + source[m, n],  accumulated in fp32 and rounded once.
+ * A has GEMM_BLOCK_ROW scales; B (N rows of K codes) has those of block_b. */
+typedef struct {
+  int64_t M, N, K;
+  int64_t lda, ldb;            /* bytes from row to row: >= K, multiples of 16, zeros behind K  */
+  int64_t scale_lda, scale_ldb; /* floats from block column to block column of the scales       */
+  int32_t block_b;             /* gemm_block                                                    */
+  int32_t pow2;                /* all scales of both operands are powers of two (or NaN): the
+                                  matrix instructions apply their exponents                     */
+  int32_t dtype_c;             /* GEMM_BF16 or GEMM_F32                                         */
+  int32_t dtype_source;        /* GEMM_BF16 or GEMM_F32; read where source is given             */
+} gemm_block_desc;
+
+int gemm_block_workspace(const gemm_block_desc *desc, size_t *bytes);
+
+/* A, B 16-byte aligned; bias (N floats) and source (M x N, packed rows; may be C) or NULL. */
+int gemm_block_run(const gemm_block_desc *desc, const void *A, const float *scale_a,
+                   const void *B, const float *scale_b, void *C, const float *bias,
+                   const void *source, void *workspace, size_t workspace_bytes, void *stream);
+
+/* Layer norm of each row of x (dtype; element (i, j) at i * stride + j) over its cols > 0 elements:
+ *   y = (x - mean) rstd w + b,  rstd = 1 / sqrt(mean((x - mean)^2) + eps);  b may be NULL.
+ * w, b: wtype, GEMM_F32 or dtype.  y: dtype, packed rows.  mean, rstd: one float a row. */
+int gemm_layer_norm(const void *x, int dtype, int64_t rows, int64_t cols, int64_t stride,
+                    const void *w, const void *b, int wtype, float eps, void *y, float *mean,
+                    float *rstd, void *stream);
+
+int gemm_layer_norm_backward_workspace(int64_t rows, int64_t cols, size_t *bytes);
+
+/* Gradients of gemm_layer_norm for the gradient dy of y: dx (dtype, packed rows), dw and db
+ * (wtype, cols elements; summed over the rows in fp32). */
+int gemm_layer_norm_backward(const void *dy, int64_t dy_stride, const void *x, int64_t x_stride,
+                             int dtype, int64_t rows, int64_t cols, const void *w, int wtype,
+                             const float *mean, const float *rstd, void *dx, void *dw, void *db,
+                             void *workspace, size_t workspace_bytes, void *stream);
+
+/* One tensor of a list of gradients: numel packed elements of dtype (GEMM_BF16 or GEMM_F32).
+ * The list itself is host memory and is not needed after the call. */
+typedef struct {
+  const void *data;
+  void *out;        /* gemm_clip_grad_norm: where the scaled tensor goes; may be data itself */
+  int64_t numel;
+  int64_t dtype;
+} gemm_tensor;
+
+int gemm_grad_norm_workspace(const gemm_tensor *list, int64_t count, size_t *bytes);
+
+/* *norm = sqrt of the sum of squares of every element of the list, summed in fp64. */
+int gemm_grad_norm(const gemm_tensor *list, int64_t count, float *norm, void *workspace,
+                   size_t workspace_bytes, void *stream);
+
+/* The same, and out = data * min(1, max_norm / (norm + 1e-6)) for every tensor. */
+int gemm_clip_grad_norm(const gemm_tensor *list, int64_t count, float max_norm, float *norm,
+                        void *workspace, size_t workspace_bytes, void *stream);
+
+#ifdef __cplusplus
+}
+#endif
+#endif

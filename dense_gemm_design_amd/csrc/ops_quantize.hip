@@ -8,9 +8,16 @@
 // an 8 x 8 corner: 16-byte loads, and eight rows that make eight bytes of a transposed row).  The
 // transposed codes go through 16 KB of LDS to leave as whole 128-byte lines.
 //
-// Rounding: the code is that of the exact quotient.  x * (1 / s) in fp32 is within 2^-22 of it, so
-// it is converted twice, moved down and up by 2^-21; only where the two codes differ (a quotient
-// next to a border between two codes) is the quotient's side of that border found exactly.
+// Rounding: the code is that of the exact quotient x / s, and x * (1 / s) in fp32 is within 2^-22 of
+// that, which matters next to a border between two codes.
+//  * A power of two divides exactly.
+//  * fp32 x: the product is converted twice, moved down and up by 2^-21; only where the two codes
+//    differ (one vector of eight in 10^4 lanes) is the quotient's side of the border found exactly.
+//  * bf16 x: quotients on a border are common (0.3 % of values), but 448 x / amax of 8-bit mantissas
+//    is either on a border or 2^-13 away, so the rounding of s alone decides: the reciprocal is moved
+//    by 2^-15 to the side that s was rounded from, and the product rounded to 17 bits, which puts
+//    those on the border exactly there where s is exact.  (8192 x 4096, both sides: 73 us by the
+//    fp32 way, where nearly every wave met a border, 27 us with powers of two.)
 //
 // Bound by memory: reads each element once and writes each code once.
 #include "../../include/gemm_ops.h"
@@ -57,19 +64,35 @@ __device__ __forceinline__ float scale_of(uint32_t amax) {
   }
 }
 
-// Reciprocal of a scale, and it moved down and up past the errors of the quotient.
-template <bool POW2>
-struct Recip {
-  float lo, hi;
-  __device__ __forceinline__ explicit Recip(float s) {
-    if constexpr (POW2) {
-      // exact: 2^-e, and NaN for NaN
-      lo = hi = s == s ? float_of(0x7F000000u - bits_of(s)) : s;
-    } else {
-      const float r = __builtin_amdgcn_rcpf(s);
-      lo = r * (1.0f - 0x1p-21f);
-      hi = r * (1.0f + 0x1p-21f);
-    }
+// How elements are divided by a scale of a block whose largest magnitude has the bits amax.
+template <class T, bool POW2>
+struct Divide;
+template <class T>
+struct Divide<T, true> {
+  float r;
+  __device__ __forceinline__ Divide(float s, uint32_t)
+      : r(s == s ? float_of(0x7F000000u - bits_of(s)) : s) {}   // exact: 2^-e, and NaN for NaN
+  __device__ __forceinline__ float operator()(float x) const { return x * r; }
+};
+template <>
+struct Divide<bf16_t, false> {
+  float r;
+  __device__ __forceinline__ Divide(float s, uint32_t amax) {
+    const float e = fmaf(-448.0f, s, float_of(amax));   // exact; s = 2^-126 divides exactly
+    r = __builtin_amdgcn_rcpf(s);
+    if (s > 0x1p-126f) r *= e > 0.0f ? 1.0f + 0x1p-15f : e < 0.0f ? 1.0f - 0x1p-15f : 1.0f;
+  }
+  __device__ __forceinline__ float operator()(float x) const {
+    return float_of((bits_of(x * r) + 0x40u) & ~0x7Fu);
+  }
+};
+template <>
+struct Divide<float, false> {
+  float s, lo, hi;
+  __device__ __forceinline__ Divide(float scale, uint32_t) : s(scale) {
+    const float r = __builtin_amdgcn_rcpf(s);
+    lo = r * (1.0f - 0x1p-21f);
+    hi = r * (1.0f + 0x1p-21f);
   }
 };
 
@@ -91,24 +114,25 @@ __device__ __noinline__ float sticky_quotient(float x, float s) {
   return float_of(u | 1u);
 }
 
-// Eight codes: element i is x[i] / s[i].
-template <bool POW2, class GetX, class GetS, class GetR>
-__device__ __forceinline__ u32x2_t codes8(GetX x, GetS s, GetR r) {
+// Eight codes: element i is x(i) divided by d.
+template <class T, bool POW2, class GetX>
+__device__ __forceinline__ u32x2_t codes8(GetX x, const Divide<T, POW2> &d) {
   u32x2_t lo;
-#pragma unroll
-  for (int h = 0; h < 2; ++h)
-    lo[h] = cvt4(x(4 * h) * r(4 * h).lo, x(4 * h + 1) * r(4 * h + 1).lo,
-                 x(4 * h + 2) * r(4 * h + 2).lo, x(4 * h + 3) * r(4 * h + 3).lo);
-  if constexpr (!POW2) {
-    u32x2_t hi;
+  if constexpr (POW2 || sizeof(T) == 2) {
 #pragma unroll
     for (int h = 0; h < 2; ++h)
-      hi[h] = cvt4(x(4 * h) * r(4 * h).hi, x(4 * h + 1) * r(4 * h + 1).hi,
-                   x(4 * h + 2) * r(4 * h + 2).hi, x(4 * h + 3) * r(4 * h + 3).hi);
+      lo[h] = cvt4(d(x(4 * h)), d(x(4 * h + 1)), d(x(4 * h + 2)), d(x(4 * h + 3)));
+  } else {
+    u32x2_t hi;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      lo[h] = cvt4(x(4 * h) * d.lo, x(4 * h + 1) * d.lo, x(4 * h + 2) * d.lo, x(4 * h + 3) * d.lo);
+      hi[h] = cvt4(x(4 * h) * d.hi, x(4 * h + 1) * d.hi, x(4 * h + 2) * d.hi, x(4 * h + 3) * d.hi);
+    }
     if (((lo[0] ^ hi[0]) | (lo[1] ^ hi[1])) != 0) {
       float q[8];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) q[i] = sticky_quotient(x(i), s(i));
+      for (int i = 0; i < 8; ++i) q[i] = sticky_quotient(x(i), d.s);
       lo[0] = cvt4(q[0], q[1], q[2], q[3]);
       lo[1] = cvt4(q[4], q[5], q[6], q[7]);
     }
@@ -164,7 +188,7 @@ __global__ void __launch_bounds__(256) quantize_kernel(const QuantArgs a) {
     __syncthreads();
     m = max(max(cmax[0][0], cmax[0][1]), max(cmax[0][2], cmax[0][3]));
     const float s = scale_of<POW2>(m);
-    const Recip<POW2> r(s);
+    const Divide<T, POW2> d(s, m);
     if (tid == 0) {
       if (SIDES & SIDE_ROWS) a.scales[ct * a.spitch + rt] = s;
       if (SIDES & SIDE_COLS) a.scales_t[rt * a.spitch_t + ct] = s;
@@ -172,8 +196,7 @@ __global__ void __launch_bounds__(256) quantize_kernel(const QuantArgs a) {
     u32x2_t c[8];
 #pragma unroll
     for (int p = 0; p < 8; ++p) {
-      c[p] = codes8<POW2>([&](int i) { return v[p].at(i); }, [&](int) { return s; },
-                          [&](int) { return r; });
+      c[p] = codes8<T, POW2>([&](int i) { return v[p].at(i); }, d);
       c[p] = p < nr ? first_bytes(c[p], nc) : u32x2_t{0, 0};
       if ((SIDES & SIDE_ROWS) && p < nr && c0 < a.pitch)
         *(u32x2_t *)(a.codes + (r0 + p) * a.pitch + c0) = c[p];
@@ -210,11 +233,10 @@ __global__ void __launch_bounds__(256) quantize_kernel(const QuantArgs a) {
       float own = 0.0f;
 #pragma unroll
       for (int p = 0; p < 8; ++p) {
-        const float s = scale_of<POW2>(row16_max(rmax[p]));
-        const Recip<POW2> r(s);
+        const uint32_t m = row16_max(rmax[p]);
+        const float s = scale_of<POW2>(m);
         own = cg == p ? s : own;
-        u32x2_t c = codes8<POW2>([&](int i) { return v[p].at(i); }, [&](int) { return s; },
-                                 [&](int) { return r; });
+        const u32x2_t c = codes8<T, POW2>([&](int i) { return v[p].at(i); }, Divide<T, POW2>(s, m));
         if (p < nr && c0 < a.pitch)
           *(u32x2_t *)(a.codes + (r0 + p) * a.pitch + c0) = first_bytes(c, nc);
       }
@@ -225,12 +247,11 @@ __global__ void __launch_bounds__(256) quantize_kernel(const QuantArgs a) {
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         const int col = cg * 8 + j;
-        const float s = scale_of<POW2>(
-            max(max(cmax[0][col], cmax[1][col]), max(cmax[2][col], cmax[3][col])));
-        const Recip<POW2> r(s);
+        const uint32_t m =
+            max(max(cmax[0][col], cmax[1][col]), max(cmax[2][col], cmax[3][col]));
+        const float s = scale_of<POW2>(m);
         if (tid < 16 && j < nc) a.scales_t[rt * a.spitch_t + c0 + j] = s;
-        u32x2_t c = codes8<POW2>([&](int i) { return v[i].at(j); }, [&](int) { return s; },
-                                 [&](int) { return r; });
+        const u32x2_t c = codes8<T, POW2>([&](int i) { return v[i].at(j); }, Divide<T, POW2>(s, m));
         *(u32x2_t *)&turned[col * 128 + (((rg >> 1) ^ (cg & 7)) << 4) + (rg & 1) * 8] =
             first_bytes(c, nr);
       }

@@ -14,7 +14,7 @@ CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libdgemm.so")
 SOURCES = [os.path.join(CSRC, name)
            for name in ("gemm.hip", "gemm_src_bf16.hip", "gemm_src_fp8.hip", "ops_block.hip",
-                        "ops_quantize.hip", "ops_norm.hip", "ops_clip.hip")]
+                        "ops_block_wide.hip", "ops_quantize.hip", "ops_norm.hip", "ops_clip.hip")]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 

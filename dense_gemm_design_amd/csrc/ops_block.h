@@ -1,0 +1,118 @@
+// The block-scaled product's arguments, epilogue and operand conversions, shared by its translation
+// units: ops_block.hip (tiles of 128 x 128 and less, the choice of kernel, the C ABI) and
+// ops_block_wide.hip (large tiles).
+#pragma once
+#include "gemm_kernel.h"
+
+namespace dg {
+
+struct BlockArgs {
+  const char *A, *B;
+  const float *sa, *sb;
+  char *C;
+  const float *bias;
+  const char *source;
+  float *partials;          // splits > 1: [split][M][N]
+  int64_t M, N;
+  int64_t lda, ldb, lsa, lsb;
+  int32_t kbytes;           // K rounded up to 16: what is read of a row
+  int32_t kb;               // blocks of 128 along K
+  int32_t mt, nt;           // tiles
+  int32_t splits;
+  int32_t out_bf16, src_bf16;
+  int32_t plain_rows;       // neither bias nor source, and rows of C in whole, aligned 16 bytes
+};
+
+// ---- epilogue ---------------------------------------------------------------------------------
+
+typedef u32x4 __attribute__((aligned(2))) u32x4_any;
+typedef u32x2 __attribute__((aligned(2))) u32x2_any;
+
+// Bias, source, rounding and store of four neighbouring outputs n .. n + 3 of row m; where N ends
+// among them, one by one.
+__device__ __forceinline__ void store_four(const BlockArgs &a, int64_t m, int64_t n, f32x4 v) {
+  const int64_t at = m * a.N + n;
+  if (n + 4 <= a.N) {
+    if (a.bias) v += __builtin_bit_cast(f32x4, *(const u32x4_any *)(a.bias + n));
+    if (a.source) {
+      if (a.src_bf16) {
+        const u32x2 s = *(const u32x2_any *)(a.source + at * 2);
+        v += f32x4{__uint_as_float(s[0] << 16), __uint_as_float(s[0] & 0xFFFF0000u),
+                   __uint_as_float(s[1] << 16), __uint_as_float(s[1] & 0xFFFF0000u)};
+      } else {
+        v += __builtin_bit_cast(f32x4, *(const u32x4_any *)(a.source + at * 4));
+      }
+    }
+    if (a.out_bf16)
+      *(u32x2_any *)(a.C + at * 2) = u32x2{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
+    else
+      *(u32x4_any *)(a.C + at * 4) = __builtin_bit_cast(u32x4, v);
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if (n + i >= a.N) break;
+    float z = v[i];
+    if (a.bias) z += a.bias[n + i];
+    if (a.source)
+      z += a.src_bf16 ? __uint_as_float((uint32_t)((const uint16_t *)a.source)[at + i] << 16)
+                      : ((const float *)a.source)[at + i];
+    if (a.out_bf16)
+      ((uint16_t *)a.C)[at + i] = (uint16_t)pack_bf16x2(z, 0.0f);
+    else
+      ((float *)a.C)[at + i] = z;
+  }
+}
+__device__ __forceinline__ void partial_four(const BlockArgs &a, int split, int64_t m, int64_t n,
+                                             f32x4 v) {
+  float *p = a.partials + ((int64_t)split * a.M + m) * a.N + n;
+  if (n + 4 <= a.N) {
+    *(u32x4_any *)p = __builtin_bit_cast(u32x4, v);
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    if (n + i < a.N) p[i] = v[i];
+}
+
+// The exponent byte of a power of two, in every byte-position the MFMA may be told to read: byte 0.
+__device__ __forceinline__ int exponent_of(float s) { return (int)(__float_as_uint(s) >> 23); }
+
+__device__ __forceinline__ f32x4 mfma_block(const i32x8 &b, const i32x8 &a) {
+  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(b, a, f32x4{0, 0, 0, 0}, 0, 0, 0, 0, 0,
+                                                          0);
+}
+__device__ __forceinline__ f32x4 mfma_block_scaled(const i32x8 &b, const i32x8 &a, const f32x4 &c,
+                                                   int eb, int ea) {
+  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(b, a, c, 0, 0, 0, eb, 0, ea);
+}
+
+// The codes of a fragment as bf16, eight a vector.
+struct BlockBf16 {
+  bf16x8 v[4];
+};
+__device__ __forceinline__ BlockBf16 widen(const i32x8 &q) {
+  typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+  BlockBf16 r;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const bf16x2 a = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(q[2 * j], 1.0f, false);
+    const bf16x2 b = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(q[2 * j], 1.0f, true);
+    const bf16x2 c = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(q[2 * j + 1], 1.0f, false);
+    const bf16x2 d = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(q[2 * j + 1], 1.0f, true);
+    r.v[j] = bf16x8{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
+  }
+  return r;
+}
+__device__ __forceinline__ f32x4 mfma_block(const BlockBf16 &b, const BlockBf16 &a) {
+  f32x4 p = {0, 0, 0, 0};
+#pragma unroll
+  for (int j = 0; j < 4; ++j) p = __builtin_amdgcn_mfma_f32_16x16x32_bf16(b.v[j], a.v[j], p, 0, 0, 0);
+  return p;
+}
+
+// 256 x 256 tiles of a bf16 C, all scales powers of two (ops_block_wide.hip): a.mt x a.nt of them, K
+// > 0 and not split.
+hipError_t launch_block_wide(const BlockArgs &a, bool rowb, hipStream_t s);
+
+}  // namespace dg

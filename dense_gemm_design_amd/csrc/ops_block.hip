@@ -16,115 +16,11 @@
 //    accumulate by itself;
 //  * an fp32 C takes four 16 x 16 x 32 bf16 MFMAs a block, at half the rate, on the codes converted
 //    in registers, which is exact; so do products of few rows, which wait for memory anyway.
-#include "gemm_kernel.h"
 #include "../../include/gemm_ops.h"
+#include "ops_block.h"
 
 namespace dg {
 namespace {
-
-struct BlockArgs {
-  const char *A, *B;
-  const float *sa, *sb;
-  char *C;
-  const float *bias;
-  const char *source;
-  float *partials;          // splits > 1: [split][M][N]
-  int64_t M, N;
-  int64_t lda, ldb, lsa, lsb;
-  int32_t kbytes;           // K rounded up to 16: what is read of a row
-  int32_t kb;               // blocks of 128 along K
-  int32_t mt, nt;           // tiles
-  int32_t splits;
-  int32_t out_bf16, src_bf16;
-};
-
-// ---- epilogue ---------------------------------------------------------------------------------
-
-typedef u32x4 __attribute__((aligned(2))) u32x4_any;
-typedef u32x2 __attribute__((aligned(2))) u32x2_any;
-
-// Bias, source, rounding and store of four neighbouring outputs n .. n + 3 of row m; where N ends
-// among them, one by one.
-__device__ __forceinline__ void store_four(const BlockArgs &a, int64_t m, int64_t n, f32x4 v) {
-  const int64_t at = m * a.N + n;
-  if (n + 4 <= a.N) {
-    if (a.bias) v += __builtin_bit_cast(f32x4, *(const u32x4_any *)(a.bias + n));
-    if (a.source) {
-      if (a.src_bf16) {
-        const u32x2 s = *(const u32x2_any *)(a.source + at * 2);
-        v += f32x4{__uint_as_float(s[0] << 16), __uint_as_float(s[0] & 0xFFFF0000u),
-                   __uint_as_float(s[1] << 16), __uint_as_float(s[1] & 0xFFFF0000u)};
-      } else {
-        v += __builtin_bit_cast(f32x4, *(const u32x4_any *)(a.source + at * 4));
-      }
-    }
-    if (a.out_bf16)
-      *(u32x2_any *)(a.C + at * 2) = u32x2{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
-    else
-      *(u32x4_any *)(a.C + at * 4) = __builtin_bit_cast(u32x4, v);
-    return;
-  }
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    if (n + i >= a.N) break;
-    float z = v[i];
-    if (a.bias) z += a.bias[n + i];
-    if (a.source)
-      z += a.src_bf16 ? __uint_as_float((uint32_t)((const uint16_t *)a.source)[at + i] << 16)
-                      : ((const float *)a.source)[at + i];
-    if (a.out_bf16)
-      ((uint16_t *)a.C)[at + i] = (uint16_t)pack_bf16x2(z, 0.0f);
-    else
-      ((float *)a.C)[at + i] = z;
-  }
-}
-__device__ __forceinline__ void partial_four(const BlockArgs &a, int split, int64_t m, int64_t n,
-                                             f32x4 v) {
-  float *p = a.partials + ((int64_t)split * a.M + m) * a.N + n;
-  if (n + 4 <= a.N) {
-    *(u32x4_any *)p = __builtin_bit_cast(u32x4, v);
-    return;
-  }
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-    if (n + i < a.N) p[i] = v[i];
-}
-
-// The exponent byte of a power of two, in every byte-position the MFMA may be told to read: byte 0.
-__device__ __forceinline__ int exponent_of(float s) { return (int)(__float_as_uint(s) >> 23); }
-
-__device__ __forceinline__ f32x4 mfma_block(const i32x8 &b, const i32x8 &a) {
-  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(b, a, f32x4{0, 0, 0, 0}, 0, 0, 0, 0, 0,
-                                                          0);
-}
-__device__ __forceinline__ f32x4 mfma_block_scaled(const i32x8 &b, const i32x8 &a, const f32x4 &c,
-                                                   int eb, int ea) {
-  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(b, a, c, 0, 0, 0, eb, 0, ea);
-}
-
-// The codes of a fragment as bf16, eight a vector.
-struct BlockBf16 {
-  bf16x8 v[4];
-};
-__device__ __forceinline__ BlockBf16 widen(const i32x8 &q) {
-  typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
-  BlockBf16 r;
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const bf16x2 a = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(q[2 * j], 1.0f, false);
-    const bf16x2 b = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(q[2 * j], 1.0f, true);
-    const bf16x2 c = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(q[2 * j + 1], 1.0f, false);
-    const bf16x2 d = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(q[2 * j + 1], 1.0f, true);
-    r.v[j] = bf16x8{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
-  }
-  return r;
-}
-__device__ __forceinline__ f32x4 mfma_block(const BlockBf16 &b, const BlockBf16 &a) {
-  f32x4 p = {0, 0, 0, 0};
-#pragma unroll
-  for (int j = 0; j < 4; ++j) p = __builtin_amdgcn_mfma_f32_16x16x32_bf16(b.v[j], a.v[j], p, 0, 0, 0);
-  return p;
-}
 
 // ---- tiles through LDS ------------------------------------------------------------------------
 
@@ -176,15 +72,18 @@ __global__ void __launch_bounds__(WGM *WGN * 64, 2) block_kernel(const BlockArgs
     const uint32_t k = (uint32_t)kb * 128;
     const bool past = k + chunk >= (uint32_t)a.kbytes;
     lds_t *const to = smem + s * STAGE + wave * 1024;
+    // rows past the edge lie past the range of the buffer: their lanes read zeros
     const uint32_t oa = past ? kOOB : voa + k, ob = past ? kOOB : vob + k;
 #pragma unroll
     for (int j = 0; j < LA; ++j)
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(ra, to + j * NW * 1024, 16, oa,
-                                               j * NW * 8 * (int32_t)a.lda, 0, 0);
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(ra, to + j * NW * 1024, 16,
+                                               oa + (uint32_t)(j * NW * 8) * (uint32_t)a.lda, 0, 0,
+                                               0);
 #pragma unroll
     for (int j = 0; j < LB; ++j)
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(rb, to + BM * 128 + j * NW * 1024, 16, ob,
-                                               j * NW * 8 * (int32_t)a.ldb, 0, 0);
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rb, to + BM * 128 + j * NW * 1024, 16,
+                                               ob + (uint32_t)(j * NW * 8) * (uint32_t)a.ldb, 0, 0,
+                                               0);
     const auto rs = make_rsrc((const char *)(sbase + kb * spitch),
                               (int64_t)scount * 4);
     __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, smem + s * STAGE + (BM + BN) * 128 + wave * 256,
@@ -194,7 +93,9 @@ __global__ void __launch_bounds__(WGM *WGN * 64, 2) block_kernel(const BlockArgs
   // consumer
   const int wm = wave / WGN, wn = wave % WGN, r16 = lane & 15, g4 = lane >> 4;
   const uint32_t x = (r16 >> 1) & 7;
-  const uint32_t c0 = ((2 * g4) ^ x) * 16, c1 = ((2 * g4 + 1) ^ x) * 16;
+  // a lane's two chunks of a row are g4 and g4 + 4, in A and B alike: reads of neighbours cost an
+  // LDS pass more
+  const uint32_t c0 = (g4 ^ x) * 16, c1 = ((g4 + 4) ^ x) * 16;
   const uint32_t arow = (wm * WM + r16) * 128, brow = BM * 128 + (wn * WN + r16) * 128;
   const uint32_t sarow = (BM + BN) * 128 + (wm * WM + r16) * 4;
   const uint32_t sbrow = (BM + BN) * 128 + (BM + wn * WN) * 4;
@@ -406,7 +307,7 @@ BlockPlan plan_of(const gemm_block_desc &d) {
   const int64_t kb = (d.K + 127) / 128;
   if (d.M <= 32) return {PLAN_FEW, 1, 1, (int32_t)((d.N + 15) / 16)};
   const int64_t t256 = ((d.M + 255) / 256) * ((d.N + 255) / 256);
-  if (t256 >= kCUs && d.dtype_c == GEMM_BF16)
+  if (t256 >= kCUs && d.dtype_c == GEMM_BF16 && kb)
     return {PLAN_256, 1, (int32_t)((d.M + 255) / 256), (int32_t)((d.N + 255) / 256)};
   // an fp32 C's codes as bf16 leave no registers for larger sub-tiles
   const int64_t mt = (d.M + 127) / 128, nt = (d.N + 127) / 128, t = mt * nt;
@@ -506,6 +407,7 @@ extern "C" int gemm_block_run(const gemm_block_desc *d, const void *A, const flo
   a.splits = p.splits;
   a.out_bf16 = d->dtype_c == GEMM_BF16;
   a.src_bf16 = d->dtype_source == GEMM_BF16;
+  a.plain_rows = !bias && !source && (d->N * (a.out_bf16 ? 2 : 4)) % 16 == 0 && !((uintptr_t)C & 15);
   const bool rowb = d->block_b == GEMM_BLOCK_ROW;
   hipStream_t s = (hipStream_t)stream;
   if (p.kind == PLAN_FEW) {
@@ -514,9 +416,9 @@ extern "C" int gemm_block_run(const gemm_block_desc *d, const void *A, const flo
     else
       launch_few<2>(a, rowb, s);
   } else if (p.kind == PLAN_256) {
-    if (d->pow2)
-      launch_tiles<256, 256, 2, 4, MODE_POW2>(a, rowb, s);
-    else
+    if (d->pow2) {
+      if (launch_block_wide(a, rowb, s) != hipSuccess) return GEMM_ERR_HIP;
+    } else
       launch_tiles<256, 256, 2, 4, MODE_FMA>(a, rowb, s);
   } else if (d->dtype_c == GEMM_F32) {
     launch_tiles<128, 128, 2, 2, MODE_EXACT>(a, rowb, s);

@@ -222,6 +222,30 @@ def test_product_large(dev, M, N, K, block, pow2):
         assert not bool(bad.any()), (out, int(bad.sum()), bad.nonzero()[0].tolist())
 
 
+@pytest.mark.parametrize("pow2", [False, True], ids=["any", "pow2"])
+@pytest.mark.parametrize("block", ["row", "tile"])
+@pytest.mark.parametrize("M,N,K", [(4090, 4104, 100), (4096, 4352, 128), (8200, 2056, 300),
+                                   (4090, 4104, 520), (256, 65800, 260)])
+def test_product_of_large_tiles(dev, M, N, K, block, pow2):
+    """Odd and even counts of k-blocks, one among them, over several tiles a workgroup; edges of
+    every kind; rows around C stay as they were."""
+    print(f"product {M}x{N}x{K} b {block} pow2={pow2}", flush=True)
+    g = gen(M + N + K)
+    a, av = operand(g, dev, M, K, "row", pow2)
+    b, bv = operand(g, dev, N, K, block, pow2)
+    av, bv = av.to(dev), bv.to(dev)
+    want = torch.mm(av, bv.t().contiguous())
+    bound = product_bound(av, bv, K, want, BF16, [])
+    for first in (8, 3):          # rows of C at a multiple of 16 bytes, and at 2 bytes
+        held = torch.full((N * 16 + M * N,), 5.0, dtype=BF16, device=dev)
+        at = N * 8 + (first - 8)
+        c = held[at:at + M * N].view(M, N)
+        dg.block_gemm(a, b, out=c)
+        bad = ~((c.double() - want).abs() <= bound)
+        assert not bool(bad.any()), (int(bad.sum()), bad.nonzero()[0].tolist())
+        assert bool((held[:at] == 5).all()) and bool((held[at + M * N:] == 5).all())
+
+
 def test_product_adds_into_its_source(dev):
     g = gen(11)
     for M, N, K in ((20, 70, 300), (200, 70, 300), (64, 130, 9000)):

@@ -1,4 +1,5 @@
-"""Builds the HIP library libdgemm.so in-tree for gfx950 with hipcc.
+"""Builds the HIP library libdgemm.so in-tree for gfx950 with hipcc, and the Python binding of the
+operators around the product, _binding.so, which calls it.
 
 Each translation unit compiles to an object of its own, all at once (the wide-wave kernels that
 read a source matrix sit in gemm_src_*.hip for this; the operators around the product in
@@ -26,6 +27,33 @@ FLAGS = [
 ]
 
 
+BINDING = os.path.join(CSRC, "binding.cpp")
+BINDING_LIB = os.path.join(HERE, "_binding.so")
+
+
+def binding_command(out):
+    """g++ on the Python binding of the operators (host code only), against torch's headers."""
+    import sysconfig
+
+    import torch
+    from torch.utils.cpp_extension import include_paths, library_paths
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall", "-fvisibility=hidden",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}"]
+    cmd += [f for d in (*include_paths(), sysconfig.get_paths()["include"]) for f in ("-isystem", d)]
+    cmd += ["-o", out, BINDING, f"-L{HERE}", "-l:libdgemm.so", "-Wl,-rpath,$ORIGIN"]
+    for d in library_paths():
+        cmd += [f"-L{d}", f"-Wl,-rpath,{d}"]
+    return cmd + ["-ltorch_python", "-ltorch_cpu", "-ltorch", "-lc10"]
+
+
+def build_binding(verbose=False):
+    cmd = binding_command(BINDING_LIB + ".tmp")
+    if verbose:
+        print(" ".join(cmd), flush=True)
+    subprocess.run(cmd, check=True)
+    os.replace(BINDING_LIB + ".tmp", BINDING_LIB)
+
+
 def build(verbose: bool = False, extra=()) -> str:
     with tempfile.TemporaryDirectory(prefix="dgemm_build_") as tmp:
         objs = [os.path.join(tmp, os.path.basename(src) + ".o") for src in SOURCES]
@@ -43,6 +71,7 @@ def build(verbose: bool = False, extra=()) -> str:
             print(" ".join(link), flush=True)
         subprocess.run(link, check=True)
     os.replace(LIB + ".tmp", LIB)
+    build_binding(verbose)
     return LIB
 
 

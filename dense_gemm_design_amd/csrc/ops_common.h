@@ -46,6 +46,10 @@ struct Vec8<bf16_t> {
     return float_of((i & 1) ? w[i / 2] & 0xFFFF0000u : w[i / 2] << 16);
   }
   __device__ __forceinline__ void load(const bf16_t *p) { w = *(const u32x4_any *)p; }
+  // a value that is not read again soon: the caches keep others instead
+  __device__ __forceinline__ void load_once(const bf16_t *p) {
+    w = __builtin_nontemporal_load((const u32x4_any *)p);
+  }
   __device__ __forceinline__ void zero() { w = u32x4_t{0, 0, 0, 0}; }
   // the first n < 8 elements, zeros behind them
   __device__ __forceinline__ void load_some(const bf16_t *p, int n) {
@@ -64,6 +68,10 @@ struct Vec8<float> {
   __device__ __forceinline__ void load(const float *p) {
     lo = *(const u32x4_any *)p;
     hi = *(const u32x4_any *)(p + 4);
+  }
+  __device__ __forceinline__ void load_once(const float *p) {
+    lo = __builtin_nontemporal_load((const u32x4_any *)p);
+    hi = __builtin_nontemporal_load((const u32x4_any *)(p + 4));
   }
   __device__ __forceinline__ void zero() { lo = hi = u32x4_t{0, 0, 0, 0}; }
   __device__ __forceinline__ void load_some(const float *p, int n) {
@@ -98,6 +106,17 @@ __device__ __forceinline__ void store8_full(bf16_t *p, const float (&v)[8]) {
   *(u32x4_any *)p = u32x4_t{bf16_pair(v[0], v[1]), bf16_pair(v[2], v[3]), bf16_pair(v[4], v[5]),
                             bf16_pair(v[6], v[7])};
 }
+__device__ __forceinline__ void store8_once(float *p, const float (&v)[8]) {
+  __builtin_nontemporal_store(
+      u32x4_t{bits_of(v[0]), bits_of(v[1]), bits_of(v[2]), bits_of(v[3])}, (u32x4_any *)p);
+  __builtin_nontemporal_store(
+      u32x4_t{bits_of(v[4]), bits_of(v[5]), bits_of(v[6]), bits_of(v[7])}, (u32x4_any *)(p + 4));
+}
+__device__ __forceinline__ void store8_once(bf16_t *p, const float (&v)[8]) {
+  __builtin_nontemporal_store(u32x4_t{bf16_pair(v[0], v[1]), bf16_pair(v[2], v[3]),
+                                      bf16_pair(v[4], v[5]), bf16_pair(v[6], v[7])},
+                              (u32x4_any *)p);
+}
 template <class T>
 __device__ __forceinline__ void store8(T *p, const float (&v)[8], int64_t n) {
   if (n >= 8) {
@@ -115,6 +134,22 @@ __device__ __forceinline__ F wave_sum(F v) {
 #pragma unroll
   for (int d = 32; d; d >>= 1) v += __shfl_xor(v, d, 64);
   return v;
+}
+// fp32: within rows of 16 lanes by rotation, then pairs of rows and halves swapped -- vector
+// instructions only, where a shuffle goes through LDS
+template <>
+__device__ __forceinline__ float wave_sum(float v) {
+#define DG_ROR(n) \
+  v += float_of((uint32_t)__builtin_amdgcn_update_dpp(0, (int)bits_of(v), 0x120 + n, 0xF, 0xF, false))
+  DG_ROR(8);
+  DG_ROR(4);
+  DG_ROR(2);
+  DG_ROR(1);
+#undef DG_ROR
+  const auto p = __builtin_amdgcn_permlane16_swap(bits_of(v), bits_of(v), false, false);
+  v = float_of(p[0]) + float_of(p[1]);
+  const auto q = __builtin_amdgcn_permlane32_swap(bits_of(v), bits_of(v), false, false);
+  return float_of(q[0]) + float_of(q[1]);
 }
 
 // Sums of N values over the WAVES waves of a workgroup.  `slot` is the LDS of one sum; a caller

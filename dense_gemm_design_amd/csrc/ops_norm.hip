@@ -64,12 +64,15 @@ __global__ void __launch_bounds__(Geo<WAVES>::THREADS) norm_kernel(const NormArg
       load8(next[v], (const T *)a.x + r * a.stride + e, a.cols - e);
     }
   };
-  if (row < a.rows) fetch(row);
+  // three vectors of fp32 leave no room for the next row's
+  constexpr bool AHEAD = NV < 3 || sizeof(T) == 2;
+  if (AHEAD && row < a.rows) fetch(row);
   for (; row < a.rows; row += step) {
+    if constexpr (!AHEAD) fetch(row);
     Vec8<T> x[NV];
 #pragma unroll
     for (int v = 0; v < NV; ++v) x[v] = next[v];
-    if (row + step < a.rows) fetch(row + step);
+    if (AHEAD && row + step < a.rows) fetch(row + step);
     float s[1] = {0.0f};
 #pragma unroll
     for (int v = 0; v < NV; ++v)
@@ -170,8 +173,8 @@ __global__ void __launch_bounds__(Geo<WAVES>::THREADS) norm_grad_kernel(const No
     }
   }
   const float inv_n = 1.0f / (float)a.cols;
-  // sixteen waves leave a thread 128 registers: no room for the next row
-  constexpr bool AHEAD = WAVES < 16;
+  // four vectors of fp32 x and dy leave no room for the next row's
+  constexpr bool AHEAD = NV < 4 || sizeof(T) == 2;
   Vec8<T> nx[NV], ng[NV];
   float nmean = 0.0f, nrstd = 0.0f;
   auto fetch = [&](int64_t r) {
@@ -324,7 +327,14 @@ __global__ void __launch_bounds__(1024)
   const int64_t col = (int64_t)blockIdx.x * 32 + c;   // of 2 x cols
   float s = 0.0f;
   if (col < 2 * cols)
-    for (int64_t r = g; r < count; r += 32) s += partials[r * 2 * cols + col];
+    for (int64_t r = g; r < count; r += 32 * 8) {
+      float v[8];
+#pragma unroll
+      for (int u = 0; u < 8; ++u)   // loads in flight together
+        v[u] = r + 32 * u < count ? partials[(r + 32 * u) * 2 * cols + col] : 0.0f;
+#pragma unroll
+      for (int u = 0; u < 8; ++u) s += v[u];
+    }
   part[g][c] = s;
   __syncthreads();
   if (g == 0 && col < 2 * cols) {
@@ -339,26 +349,36 @@ __global__ void __launch_bounds__(1024)
 }
 
 constexpr int kCUs = 256;
-constexpr int64_t kLong = 1024 * 8 * 2;   // the longest row held in registers
+constexpr int64_t kLong = 1024 * 8 * 3, kGradLong = 512 * 8 * 4;   // the longest rows in registers
 
-// Workgroups of a backward pass: enough bytes in flight to fill the memory's pipes, few enough
-// that the partial sums stay a small part of what is moved.
+// Workgroups of a backward pass: one a CU.  515 x 1111 fp32 takes 17.6 us on 64, 11.8 on 128, 9.8 on
+// 256, 10.5 on 512 (more partial sums to join); 16384 x 4096 bf16 273, 141, 79.6 and 80.9 us.
 int grad_groups(int64_t rows, int64_t cols) {
   const int64_t per = cols <= 1024 ? 4 : 1;
   const int64_t need = (rows + per - 1) / per;
-  const int64_t most = cols <= 4096 ? 2 * kCUs : kCUs;
-  return (int)(need < most ? need : most);
+  return (int)(need < kCUs ? need : kCUs);
 }
 
-// How many waves hold a row, and as how many vectors a thread.
-#define DG_NORM_SHAPES(KERNEL, cols)                                   \
-  do {                                                                 \
-    if ((cols) <= 512) KERNEL(1, 1);                                   \
-    else if ((cols) <= 1024) KERNEL(1, 2);                             \
-    else if ((cols) <= 2048) KERNEL(4, 1);                             \
-    else if ((cols) <= 4096) KERNEL(4, 2);                             \
-    else if ((cols) <= 8192) KERNEL(8, 2);                             \
-    else KERNEL(16, 2);                                                \
+// How many waves hold a row, and as how many vectors of eight a thread: one wave up to 1024 columns
+// (no barrier), then few enough vectors that the next row's loads find registers beside this one's.
+#define DG_NORM_SHAPES(KERNEL, cols)          \
+  do {                                        \
+    if ((cols) <= 512) KERNEL(1, 1);          \
+    else if ((cols) <= 1024) KERNEL(1, 2);    \
+    else if ((cols) <= 2048) KERNEL(4, 1);    \
+    else if ((cols) <= 4096) KERNEL(4, 2);    \
+    else if ((cols) <= 8192) KERNEL(8, 2);    \
+    else if ((cols) <= 16384) KERNEL(16, 2);  \
+    else KERNEL(16, 3);                       \
+  } while (0)
+#define DG_NORM_GRAD_SHAPES(KERNEL, cols)     \
+  do {                                        \
+    if ((cols) <= 512) KERNEL(1, 1);          \
+    else if ((cols) <= 1024) KERNEL(1, 2);    \
+    else if ((cols) <= 2048) KERNEL(4, 1);    \
+    else if ((cols) <= 4096) KERNEL(4, 2);    \
+    else if ((cols) <= 8192) KERNEL(8, 2);    \
+    else KERNEL(8, 4);                        \
   } while (0)
 
 template <class T, class W>
@@ -371,7 +391,7 @@ void launch_norm(const NormArgs &a, hipStream_t s) {
 #define DG_RUN(WV, NV)                                                                        \
   do {                                                                                        \
     const int64_t need = (a.rows + Geo<WV>::ROWS - 1) / Geo<WV>::ROWS;                        \
-    const int64_t most = kCUs * (2048 / Geo<WV>::THREADS);                                    \
+    const int64_t most = kCUs * (1024 / Geo<WV>::THREADS);                                    \
     hipLaunchKernelGGL((norm_kernel<T, W, WV, NV>), dim3((uint32_t)(need < most ? need : most)), \
                        dim3(Geo<WV>::THREADS), 0, s, a);                                      \
   } while (0)
@@ -383,13 +403,13 @@ template <class T, class W>
 void launch_norm_grad(const NormArgs &a, W *dw, W *db, hipStream_t s) {
   const int grid = grad_groups(a.rows, a.cols);
   if (grid) {
-    if (a.cols > kLong) {
+    if (a.cols > kGradLong) {
       hipLaunchKernelGGL((norm_grad_long_kernel<T, W>), dim3(grid), dim3(1024), 0, s, a);
     } else {
 #define DG_RUN(WV, NV)                                                                      \
   hipLaunchKernelGGL((norm_grad_kernel<T, W, WV, NV>), dim3(grid), dim3(Geo<WV>::THREADS), 0, \
                      s, a)
-      DG_NORM_SHAPES(DG_RUN, a.cols);
+      DG_NORM_GRAD_SHAPES(DG_RUN, a.cols);
 #undef DG_RUN
     }
   }

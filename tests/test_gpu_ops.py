@@ -488,6 +488,21 @@ def test_clip_at_any_alignment(dev):
     assert float(flat[20000]) == float(flat[20000]) and bool(torch.isfinite(flat32).all())
 
 
+@pytest.mark.parametrize("into", [False, True], ids=["in_place", "into"])
+def test_clip_of_a_list_longer_than_the_caches(dev, into):
+    torch.manual_seed(32)
+    grads = [(torch.randn(n, device=dev) * 0.1).to(t)
+             for n, t in ((20_000_003, BF16), (12_345_677, F32), (17, BF16), (9_000_000, F32))]
+    before = [t.clone() for t in grads]
+    out = [torch.empty_like(t) for t in grads] if into else None
+    want = sum(float((t.double() ** 2).sum()) for t in before) ** 0.5
+    norm = dg.clip_grad_norm(grads, 0.5, out=out)
+    assert abs(float(norm) - want) <= 2 * U * want
+    for o, t in zip(out or grads, before):
+        v = t.double() * (0.5 / (want + 1e-6))
+        assert bool(((o.double() - v).abs() <= v.abs() * (6 * U + R.HALF[t.dtype])).all())
+
+
 def test_clip_of_large_squares_and_of_nothing(dev):
     big = [torch.full((1000,), 1e30, device=dev)]
     want = 1e30 * 1000 ** 0.5

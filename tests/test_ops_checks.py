@@ -208,7 +208,7 @@ def test_workspaces_cover_their_sums():
     for sizes in ([0], [1], [16384], [16385], [1] * 129, [10 ** 9] * 3):
         arr = (O.GemmTensor * len(sizes))(*[O.GemmTensor(P, P, s, 2) for s in sizes])
         assert lib.gemm_grad_norm_workspace(arr, len(sizes), ctypes.byref(n)) == 0
-        assert n.value <= 8 * sum(R.up(s, 16384) for s in sizes)
+        assert n.value <= 8 * sum(R.up(s, 2048) for s in sizes)
         assert (n.value == 0) == (sum(sizes) == 0)
 
 

@@ -53,11 +53,18 @@ def build_binding(verbose=False):
     subprocess.run(cmd, check=True)
     os.replace(BINDING_LIB + ".tmp", BINDING_LIB)
 
+# of one source: the results of its MFMAs go to the registers that vector instructions read
+FLAGS_OF = {"ops_block_wide.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"]}
+
+
+def compile_command(src, obj, extra=()):
+    return [HIPCC, *FLAGS, *FLAGS_OF.get(os.path.basename(src), ()), *extra, "-c", "-o", obj, src]
+
 
 def build(verbose: bool = False, extra=()) -> str:
     with tempfile.TemporaryDirectory(prefix="dgemm_build_") as tmp:
         objs = [os.path.join(tmp, os.path.basename(src) + ".o") for src in SOURCES]
-        cmds = [[HIPCC, *FLAGS, *extra, "-c", "-o", obj, src] for src, obj in zip(SOURCES, objs)]
+        cmds = [compile_command(src, obj, extra) for src, obj in zip(SOURCES, objs)]
         for cmd in cmds:
             if verbose:
                 print(" ".join(cmd), flush=True)

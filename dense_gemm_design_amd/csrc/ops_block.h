@@ -20,7 +20,7 @@ struct BlockArgs {
   int32_t mt, nt;           // tiles
   int32_t splits;
   int32_t out_bf16, src_bf16;
-  int32_t plain_rows;       // neither bias nor source, and rows of C in whole, aligned 16 bytes
+  int32_t plain_rows;       // no source, and rows of C in whole, aligned 16 bytes
 };
 
 // ---- epilogue ---------------------------------------------------------------------------------
@@ -111,8 +111,9 @@ __device__ __forceinline__ f32x4 mfma_block(const BlockBf16 &b, const BlockBf16 
   return p;
 }
 
-// 256 x 256 tiles of a bf16 C, all scales powers of two (ops_block_wide.hip): a.mt x a.nt of them, K
-// > 0 and not split.
-hipError_t launch_block_wide(const BlockArgs &a, bool rowb, hipStream_t s);
+// Large tiles of a bf16 C (ops_block_wide.hip), wide_rows() x 256: a.mt x a.nt of them, K > 0 and not
+// split.  All scales are powers of two, or B's are of 128 x 128 blocks.
+constexpr int wide_rows(bool pow2) { return pow2 ? 256 : 192; }
+hipError_t launch_block_wide(const BlockArgs &a, bool rowb, bool pow2, hipStream_t s);
 
 }  // namespace dg

@@ -105,6 +105,8 @@ __global__ void __launch_bounds__(WGM *WGN * 64, 2) block_kernel(const BlockArgs
   for (int f = 0; f < FM; ++f)
 #pragma unroll
     for (int g = 0; g < FN; ++g) acc[f][g] = f32x4{0, 0, 0, 0};
+  // a wave wholly past the edge only loads
+  const bool inside = m0 + wm * WM < a.M && n0 + wn * WN < a.N;
 
   if (kb0 < kb1) load_stage(kb0, 0);
   for (int32_t kb = kb0; kb < kb1; ++kb) {
@@ -113,6 +115,7 @@ __global__ void __launch_bounds__(WGM *WGN * 64, 2) block_kernel(const BlockArgs
     // the barrier that holds for every wave
     asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
     if (kb + 1 < kb1) load_stage(kb + 1, s ^ 1);
+    if (!inside) continue;
     const lds_t *const st = smem + s * STAGE;
     typedef const float __attribute__((address_space(3))) *fp;
     typedef const f32x4 __attribute__((address_space(3))) *f4p;
@@ -197,15 +200,23 @@ __global__ void __launch_bounds__(256) join_kernel(const BlockArgs a) {
   for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < all; i += (int64_t)gridDim.x * 256) {
     const int64_t m = i / per_row, n = i % per_row * 4;
     f32x4 v = {0, 0, 0, 0};
-    for (int s = 0; s < a.splits; ++s) {
-      const float *p = a.partials + ((int64_t)s * a.M + m) * a.N + n;
-      if (n + 4 <= a.N) {
-        v += __builtin_bit_cast(f32x4, *(const u32x4_any *)p);
-      } else {
+    for (int s = 0; s < a.splits; s += 4) {
+      f32x4 q[4];   // loads in flight together
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-          if (n + e < a.N) v[e] += p[e];
+      for (int u = 0; u < 4; ++u) {
+        const float *p = a.partials + ((int64_t)(s + u) * a.M + m) * a.N + n;
+        q[u] = f32x4{0, 0, 0, 0};
+        if (s + u >= a.splits) continue;
+        if (n + 4 <= a.N) {
+          q[u] = __builtin_bit_cast(f32x4, *(const u32x4_any *)p);
+        } else {
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if (n + e < a.N) q[u][e] = p[e];
+        }
       }
+#pragma unroll
+      for (int u = 0; u < 4; ++u) v += q[u];
     }
     store_four(a, m, n, v);
   }
@@ -297,7 +308,7 @@ __global__ void __launch_bounds__(512) few_kernel(const BlockArgs a) {
 
 constexpr int kCUs = 256;
 
-enum { PLAN_FEW, PLAN_128, PLAN_256 };
+enum { PLAN_FEW, PLAN_128, PLAN_256, PLAN_WIDE };
 struct BlockPlan {
   int kind, splits;
   int32_t mt, nt;
@@ -306,16 +317,43 @@ struct BlockPlan {
 BlockPlan plan_of(const gemm_block_desc &d) {
   const int64_t kb = (d.K + 127) / 128;
   if (d.M <= 32) return {PLAN_FEW, 1, 1, (int32_t)((d.N + 15) / 16)};
-  const int64_t t256 = ((d.M + 255) / 256) * ((d.N + 255) / 256);
-  if (t256 >= kCUs && d.dtype_c == GEMM_BF16 && kb)
-    return {PLAN_256, 1, (int32_t)((d.M + 255) / 256), (int32_t)((d.N + 255) / 256)};
-  // an fp32 C's codes as bf16 leave no registers for larger sub-tiles
+  if (d.dtype_c == GEMM_BF16 && kb) {
+    // Tiles of 256 x 256 (wide with powers of two, eight waves otherwise) or, for fp32 scales of 128 x
+    // 128 blocks, wide ones of 192 x 256, whose round over the CUs takes 0.74 as long: 8192^3 542 us on
+    // six rounds of them, 498 on four of 256; 4096 x 14336 x 4096 237 us on five, 263 on four.
+    const auto rounds = [&](int rows) {
+      return (((d.M + rows - 1) / rows) * ((d.N + 255) / 256) + kCUs - 1) / kCUs;
+    };
+    const bool fp32_tiles = !d.pow2 && d.block_b == GEMM_BLOCK_TILE;
+    const bool narrow = fp32_tiles && 0.74 * rounds(wide_rows(false)) < rounds(256);
+    const int rows = narrow ? wide_rows(false) : 256;
+    const int64_t mt = (d.M + rows - 1) / rows, nt = (d.N + 255) / 256;
+    if (mt * nt >= kCUs)
+      return {d.pow2 || narrow ? PLAN_WIDE : PLAN_256, 1, (int32_t)mt, (int32_t)nt};
+  }
+  // Tiles of 128 x 128 (an fp32 C's codes as bf16 leave no registers for larger sub-tiles), two
+  // workgroups a CU, and K cut so that the estimate below is least.  A k-block takes a CU c1 us with
+  // one workgroup and c2 with two: 1.29 and 2.1 measured with an fp32 C, 1.0 and 1.38 with bf16.  What
+  // the pieces leave costs 8 bytes an element and piece to write and read, and a launch.  (us on one,
+  // two, three, four, six pieces: 1000 x 4104 x 8201 fp32 136, 118, 107, 105, 107; 256 x 4096 x 4096
+  // bf16 28, 23, 20, 19, 21; 64 x 16384 x 16384 bf16 108, 68, 57, 52, 64.)
   const int64_t mt = (d.M + 127) / 128, nt = (d.N + 127) / 128, t = mt * nt;
-  // too few tiles for two workgroups a CU: K is cut, in pieces of four blocks at least
-  int64_t splits = 2 * kCUs / t;
-  if (splits > kb / 4) splits = kb / 4;
-  if (splits < 1) splits = 1;
-  return {PLAN_128, (int)splits, (int32_t)mt, (int32_t)nt};
+  const bool f32 = d.dtype_c == GEMM_F32;
+  const double c1 = f32 ? 1.29 : 1.0, c2 = f32 ? 2.1 : 1.38;
+  int splits = 1;
+  double least = 0.0;
+  for (int s = 1; s <= 64 && (s == 1 || (s * 2 <= kb && t * s <= 8 * kCUs)); ++s) {
+    const double groups = (double)t * s, blocks = (double)((kb + s - 1) / s);
+    double us = groups <= kCUs ? blocks * c1
+                : groups <= 2 * kCUs ? blocks * c2
+                                     : (groups / (2 * kCUs) + 0.5) * blocks * c2;
+    if (s > 1) us += 3.0 + (double)d.M * (double)d.N * 8e-6 / 8.0 * s;
+    if (s == 1 || us < least) {
+      least = us;
+      splits = s;
+    }
+  }
+  return {PLAN_128, splits, (int32_t)mt, (int32_t)nt};
 }
 
 template <int BM, int BN, int WGM, int WGN, int MODE>
@@ -407,7 +445,7 @@ extern "C" int gemm_block_run(const gemm_block_desc *d, const void *A, const flo
   a.splits = p.splits;
   a.out_bf16 = d->dtype_c == GEMM_BF16;
   a.src_bf16 = d->dtype_source == GEMM_BF16;
-  a.plain_rows = !bias && !source && (d->N * (a.out_bf16 ? 2 : 4)) % 16 == 0 && !((uintptr_t)C & 15);
+  a.plain_rows = !source && (d->N * (a.out_bf16 ? 2 : 4)) % 16 == 0 && !((uintptr_t)C & 15);
   const bool rowb = d->block_b == GEMM_BLOCK_ROW;
   hipStream_t s = (hipStream_t)stream;
   if (p.kind == PLAN_FEW) {
@@ -416,10 +454,9 @@ extern "C" int gemm_block_run(const gemm_block_desc *d, const void *A, const flo
     else
       launch_few<2>(a, rowb, s);
   } else if (p.kind == PLAN_256) {
-    if (d->pow2) {
-      if (launch_block_wide(a, rowb, s) != hipSuccess) return GEMM_ERR_HIP;
-    } else
-      launch_tiles<256, 256, 2, 4, MODE_FMA>(a, rowb, s);
+    launch_tiles<256, 256, 2, 4, MODE_FMA>(a, rowb, s);
+  } else if (p.kind == PLAN_WIDE) {
+    if (launch_block_wide(a, rowb, d->pow2 != 0, s) != hipSuccess) return GEMM_ERR_HIP;
   } else if (d->dtype_c == GEMM_F32) {
     launch_tiles<128, 128, 2, 2, MODE_EXACT>(a, rowb, s);
   } else if (d->pow2) {

@@ -224,23 +224,29 @@ __global__ void __launch_bounds__(256) join_kernel(const BlockArgs a) {
 
 // ---- few rows ---------------------------------------------------------------------------------
 
-// Up to 16 FM rows of A: what counts is to read B once at the memory's rate.  A workgroup takes 16
-// rows of B (16 columns of C); its eight waves take every eighth k-block straight into registers,
-// and their sums meet in LDS.
-constexpr int kAhead = 4;   // k-blocks of a wave whose loads are in flight together
-template <int FM, bool ROWB>
+// Up to 16 FM rows of A: what counts is to read B once at the memory's rate.  A workgroup takes 16 GN
+// rows of B (columns of C); its eight waves take every eighth k-block (of its piece of K) straight
+// into registers, and their sums meet in LDS.  1 x 4096 x 4096 takes 5.9 us on the GPU, 6.7 with
+// sixteen waves; 1 x 16384 x 16384 52.6 us, 5.1 TB/s.
+template <int FM, int GN, bool ROWB>
 __global__ void __launch_bounds__(512) few_kernel(const BlockArgs a) {
-  __shared__ float part[8][FM][16][17];
+  constexpr int WAVES = 8;
+  constexpr int AHEAD = FM * GN > 2 ? 2 : 4;   // k-blocks of a wave whose loads are in flight together
+  __shared__ float part[WAVES][FM][GN][16][17];
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
   const int r16 = lane & 15, g4 = lane >> 4;
-  const int64_t n0 = (int64_t)blockIdx.x * 16;
+  const int64_t n0 = (int64_t)blockIdx.x * (16 * GN);
   const auto ra = make_rsrc(a.A, a.M * a.lda);
-  const int64_t rows_b = a.N - n0 < 16 ? a.N - n0 : 16;
+  const int64_t rows_b = a.N - n0 < 16 * GN ? a.N - n0 : 16 * GN;
   const auto rb = make_rsrc(a.B + n0 * a.ldb, rows_b * a.ldb);
-  f32x4 acc[FM];
+  const int split = blockIdx.y;
+  const int32_t kb1 = (int32_t)((int64_t)a.kb * (split + 1) / a.splits);
+  f32x4 acc[FM][GN];
 #pragma unroll
-  for (int f = 0; f < FM; ++f) acc[f] = f32x4{0, 0, 0, 0};
-  // past K, and past the last k-block, an operand reads as zeros
+  for (int f = 0; f < FM; ++f)
+#pragma unroll
+    for (int g = 0; g < GN; ++g) acc[f][g] = f32x4{0, 0, 0, 0};
+  // past K an operand reads as zeros
   auto take = [&](auto r, uint32_t row, uint32_t ld, uint32_t k) {
     const uint32_t o0 = k < (uint32_t)a.kbytes ? row * ld + k : kOOB;
     const uint32_t o1 = k + 16 < (uint32_t)a.kbytes ? row * ld + k + 16 : kOOB;
@@ -248,59 +254,76 @@ __global__ void __launch_bounds__(512) few_kernel(const BlockArgs a) {
     const i32x4 hi = __builtin_bit_cast(i32x4, __builtin_amdgcn_raw_buffer_load_b128(r, o1, 0, 0));
     return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
   };
-  for (int32_t kb0 = wave; kb0 < a.kb; kb0 += 8 * kAhead) {
-    i32x8 b[kAhead], x[kAhead][FM];
-    float s[kAhead][FM];
-    f32x4 sb[kAhead];
+  for (int32_t kb0 = (int32_t)((int64_t)a.kb * split / a.splits) + wave; kb0 < kb1;
+       kb0 += WAVES * AHEAD) {
+    i32x8 b[AHEAD][GN], x[AHEAD][FM];
+    float s[AHEAD][FM];
+    f32x4 sb[AHEAD][GN];
 #pragma unroll
-    for (int u = 0; u < kAhead; ++u) {
-      const int32_t kb = kb0 + 8 * u;
-      const bool in = kb < a.kb;
-      const uint32_t k = (uint32_t)kb * 128 + g4 * 32;
-      b[u] = take(rb, r16, (uint32_t)a.ldb, k);
+    for (int u = 0; u < AHEAD; ++u) {
+      const int32_t kb = kb0 + WAVES * u;
+      const bool in = kb < kb1;   // past the last k-block too
+      const uint32_t k = in ? (uint32_t)kb * 128 + g4 * 32 : (uint32_t)a.kbytes;
+#pragma unroll
+      for (int g = 0; g < GN; ++g) b[u][g] = take(rb, g * 16 + r16, (uint32_t)a.ldb, k);
 #pragma unroll
       for (int f = 0; f < FM; ++f) {
         const int64_t m = f * 16 + r16;
         x[u][f] = take(ra, (uint32_t)m, (uint32_t)a.lda, k);
         s[u][f] = in && m < a.M ? a.sa[kb * a.lsa + m] : 0.0f;
       }
-      if constexpr (ROWB) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int64_t n = n0 + g4 * 4 + e;
-          sb[u][e] = in && n < a.N ? a.sb[kb * a.lsb + n] : 0.0f;
+      for (int g = 0; g < GN; ++g) {
+        if constexpr (ROWB) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int64_t n = n0 + g * 16 + g4 * 4 + e;
+            sb[u][g][e] = in && n < a.N ? a.sb[kb * a.lsb + n] : 0.0f;
+          }
+        } else {
+          const float z = in ? a.sb[kb * a.lsb + n0 / 128] : 0.0f;
+          sb[u][g] = f32x4{z, z, z, z};
         }
-      } else {
-        const float z = in ? a.sb[kb * a.lsb + n0 / 128] : 0.0f;
-        sb[u] = f32x4{z, z, z, z};
       }
     }
 #pragma unroll
-    for (int u = 0; u < kAhead; ++u) {
-      const BlockBf16 wide = widen(b[u]);
+    for (int u = 0; u < AHEAD; ++u) {
+      BlockBf16 wide[GN];
+#pragma unroll
+      for (int g = 0; g < GN; ++g) wide[g] = widen(b[u][g]);
 #pragma unroll
       for (int f = 0; f < FM; ++f) {
-        const f32x4 p = mfma_block(wide, widen(x[u][f]));
+        const BlockBf16 w = widen(x[u][f]);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) acc[f][e] = fmaf(p[e], s[u][f] * sb[u][e], acc[f][e]);
+        for (int g = 0; g < GN; ++g) {
+          const f32x4 p = mfma_block(wide[g], w);
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            acc[f][g][e] = fmaf(p[e], s[u][f] * sb[u][g][e], acc[f][g][e]);
+        }
       }
     }
   }
 #pragma unroll
   for (int f = 0; f < FM; ++f)
 #pragma unroll
-    for (int e = 0; e < 4; ++e) part[wave][f][r16][g4 * 4 + e] = acc[f][e];
+    for (int g = 0; g < GN; ++g)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) part[wave][f][g][r16][g4 * 4 + e] = acc[f][g][e];
   __syncthreads();
-  for (int i = threadIdx.x; i < FM * 64; i += 512) {
-    const int f = i / 64, m16 = (i / 4) % 16, q = i % 4;
-    const int64_t m = f * 16 + m16, n = n0 + q * 4;
+  for (int i = threadIdx.x; i < FM * GN * 64; i += WAVES * 64) {
+    const int f = i / (64 * GN), g = i / 64 % GN, m16 = i / 4 % 16, q = i % 4;
+    const int64_t m = f * 16 + m16, n = n0 + g * 16 + q * 4;
     if (m >= a.M || n >= a.N) continue;
     f32x4 v = {0, 0, 0, 0};
 #pragma unroll
-    for (int w = 0; w < 8; ++w)
+    for (int w = 0; w < WAVES; ++w)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) v[e] += part[w][f][m16][q * 4 + e];
-    store_four(a, m, n, v);
+      for (int e = 0; e < 4; ++e) v[e] += part[w][f][g][m16][q * 4 + e];
+    if (a.splits > 1)
+      partial_four(a, split, m, n, v);
+    else
+      store_four(a, m, n, v);
   }
 }
 
@@ -314,9 +337,20 @@ struct BlockPlan {
   int32_t mt, nt;
 };
 
+int few_columns(const gemm_block_desc &d) { return d.M > 16 && d.N > 16 * kCUs ? 32 : 16; }
+
 BlockPlan plan_of(const gemm_block_desc &d) {
   const int64_t kb = (d.K + 127) / 128;
-  if (d.M <= 32) return {PLAN_FEW, 1, 1, (int32_t)((d.N + 15) / 16)};
+  if (d.M <= 32) {
+    // 32 columns a workgroup where there are more rows of A to read beside them than one block's and
+    // columns enough (32 x 16384 x 16384 69 us, 97 on 16; 32 x 4096 x 4096 10.8, 8.8); K in pieces where
+    // there are few columns and much of it
+    const int cols = few_columns(d);
+    const int64_t nt = (d.N + cols - 1) / cols;
+    int64_t splits = nt < 128 ? 256 / nt : 1;
+    if (splits > kb / 16) splits = kb / 16;
+    return {PLAN_FEW, splits > 1 ? (int)splits : 1, 1, (int32_t)nt};
+  }
   if (d.dtype_c == GEMM_BF16 && kb) {
     // Tiles of 256 x 256 (wide with powers of two, eight waves otherwise) or, for fp32 scales of 128 x
     // 128 blocks, wide ones of 192 x 256, whose round over the CUs takes 0.74 as long: 8192^3 542 us on
@@ -364,12 +398,13 @@ void launch_tiles(const BlockArgs &a, bool rowb, hipStream_t s) {
   else
     hipLaunchKernelGGL((block_kernel<BM, BN, WGM, WGN, false, MODE>), grid, block, 0, s, a);
 }
-template <int FM>
+template <int FM, int GN>
 void launch_few(const BlockArgs &a, bool rowb, hipStream_t s) {
+  const dim3 grid((uint32_t)a.nt, (uint32_t)a.splits), block(512);
   if (rowb)
-    hipLaunchKernelGGL((few_kernel<FM, true>), dim3(a.nt), dim3(512), 0, s, a);
+    hipLaunchKernelGGL((few_kernel<FM, GN, true>), grid, block, 0, s, a);
   else
-    hipLaunchKernelGGL((few_kernel<FM, false>), dim3(a.nt), dim3(512), 0, s, a);
+    hipLaunchKernelGGL((few_kernel<FM, GN, false>), grid, block, 0, s, a);
 }
 
 int check(const gemm_block_desc *d) {
@@ -450,9 +485,11 @@ extern "C" int gemm_block_run(const gemm_block_desc *d, const void *A, const flo
   hipStream_t s = (hipStream_t)stream;
   if (p.kind == PLAN_FEW) {
     if (d->M <= 16)
-      launch_few<1>(a, rowb, s);
+      launch_few<1, 1>(a, rowb, s);
+    else if (few_columns(*d) == 16)
+      launch_few<2, 1>(a, rowb, s);
     else
-      launch_few<2>(a, rowb, s);
+      launch_few<2, 2>(a, rowb, s);
   } else if (p.kind == PLAN_256) {
     launch_tiles<256, 256, 2, 4, MODE_FMA>(a, rowb, s);
   } else if (p.kind == PLAN_WIDE) {

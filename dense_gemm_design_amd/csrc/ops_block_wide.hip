@@ -6,11 +6,14 @@
 // two rows of blocks are taken column by column, so that the reads of B's fragments have 16 slots,
 // about what LDS takes for them, and 14 more before their next MFMA.
 //  * Powers of two, 256 x 256: the 256 accumulators of a lane stay in accumulation registers, and
-//    the MFMA adds to them.
+//    the MFMA adds to them.  8192^3 in 380 us, 2.9 PFLOP/s; the matrix units are busy 0.66 of the time
+//    at the 2.05 GHz that the card then holds.
 //  * fp32 scales of 128 x 128 blocks of B, 192 x 256: vector instructions reach only the other 256
 //    registers, so there the 192 accumulators have to be, and the fragments go to the accumulation
 //    registers.  A wave's columns are one block of B, so its scales are one a row.  An MFMA's four
-//    results are added two slots later, when they have left the matrix unit.
+//    results are added two slots later, when they have left the matrix unit.  4096 x 14336 x 4096 in
+//    228 us, 2.1 PFLOP/s: with one wave a SIMD an instruction takes four cycles to issue, and the 430
+//    of a step, 192 of them these additions, take longer than its 48 MFMAs.
 // Workgroups stay for tile after tile: the loads of the next one are under way when a tile ends, and
 // what a tile leaves in the registers is written out beside the next one's first step (written at
 // once by all CUs, the 33 MB of a round took 8 us in which nothing was multiplied).
@@ -201,7 +204,7 @@ wide_block_kernel(const BlockArgs a) {
   const int wm = wave / 2, wn = wave % 2, r16 = lane & 15, g4 = lane >> 4;
 
   // ---- producer: the k-block to load next, and where its tile lies
-  struct Scales {   // of the wave's rows and columns in one k-block, and how many there are
+  struct Scales {   // of the wave's rows and columns in one k-block, and how many bytes of them there are
     const float *a, *b;
     int32_t rows, cols;
   };
@@ -221,8 +224,8 @@ wide_block_kernel(const BlockArgs a) {
       rb = make_rsrc(a.B + n0 * a.ldb, rows_b * a.ldb);
       // a sub-tile wholly past the edge reads no scales, from the start of the tile's
       const int32_t rm = rows_a - wm * WM, rn = rows_b - wn * WN;
-      ps.rows = rm > 0 ? rm : 0;
-      ps.cols = rn > 0 ? (ROWB ? rn : 1) : 0;
+      ps.rows = __builtin_amdgcn_readfirstlane(rm > 0 ? rm * 4 : 0);
+      ps.cols = __builtin_amdgcn_readfirstlane(rn > 0 ? (ROWB ? rn : 1) * 4 : 0);
       ps.a = a.sa + m0 + (rm > 0 ? wm * WM : 0);
       ps.b = a.sb + (ROWB ? n0 + (rn > 0 ? wn * WN : 0) : n0 / 128 + (rn > 0 ? wn : 0));
     } else {   // empty ranges read as zeros
@@ -282,8 +285,8 @@ wide_block_kernel(const BlockArgs a) {
   };
   __amdgpu_buffer_rsrc_t rsa, rsb;
   auto scales_at = [&](const Scales &s) {
-    rsa = make_rsrc((const char *)s.a, (int64_t)__builtin_amdgcn_readfirstlane(s.rows) * 4);
-    rsb = make_rsrc((const char *)s.b, (int64_t)__builtin_amdgcn_readfirstlane(s.cols) * 4);
+    rsa = __builtin_amdgcn_make_buffer_rsrc((void *)s.a, (short)0, s.rows, 0x00020000);
+    rsb = __builtin_amdgcn_make_buffer_rsrc((void *)s.b, (short)0, s.cols, 0x00020000);
   };
   auto read_scale = [&](int j) {
     if (j < XB)
@@ -359,10 +362,12 @@ wide_block_kernel(const BlockArgs a) {
   //    4 on.  They come into use when they have arrived and this step is done with the ones before: the
   //    first four rows' (columns') of blocks in its last slots, the others' in slots 2 and 3 of their
   //    own step;
-  //  * the handshake, after slot HS; then reads of step c + 1 and loads of step c + 2.
+  //  * the handshake, after slot HS; then reads of step c + 1 and loads of step c + 2.  (After slot 7,
+  //    11, 15, 19, 23, 31: 8192^3 with powers of two 402, 392, 383, 380, 379, 385 us -- the loads have
+  //    longer to land, the reads less time.)
   using Paired = Order<FM, true>;
   using Rows = Order<FM, false>;
-  constexpr int HS = 7, LW = HS + 1 + (NM - HS) / 2;
+  constexpr int HS = 19, LW = HS + 1 + (NM - HS) * 3 / 4;
   auto kstep = [&](auto first_c, auto pending_c) {
     constexpr bool FIRST = decltype(first_c)::value, PENDING = decltype(pending_c)::value;
     using O = std::conditional_t<FIRST, Rows, Paired>;
@@ -397,7 +402,11 @@ wide_block_kernel(const BlockArgs a) {
             if constexpr (ROWB && i == NM - 3) use_b(0);
             if constexpr (i == HS) handshake(c + 1);
             if constexpr (i >= HS) {
-              if constexpr (O::last_of_row(f) == i) read_a(next, f);
+              // (rows that were done before it at the handshake)
+              [&]<int... F>(std::integer_sequence<int, F...>) {
+                (((O::last_of_row(F) > HS ? O::last_of_row(F) : HS) == i ? read_a(next, F) : void()),
+                 ...);
+              }(std::make_integer_sequence<int, FM>());
               if constexpr (O::last_of_col(g) == i) read_b(next, g);
               constexpr int plo = ops_before(i, L, HS, LW), phi = ops_before(i + 1, L, HS, LW);
               [&]<int... J>(std::integer_sequence<int, J...>) {

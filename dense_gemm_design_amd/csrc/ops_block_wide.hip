@@ -318,8 +318,10 @@ wide_block_kernel(const BlockArgs a) {
   };
 
   int c = 0;
-  auto handshake = [&](int step) {
-    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+  // LATER: loads that were issued after the operands' and need not have arrived
+  auto handshake = [&](int step, auto later_c) {
+    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(decltype(later_c)::value)
+                 : "memory");
     begin((step + 1) & 1);
   };
   producer_tile();
@@ -327,7 +329,7 @@ wide_block_kernel(const BlockArgs a) {
   load_all();
   Scales cs = ps;   // of the step whose fragments are read next
   end();
-  handshake(0);
+  handshake(0, std::integral_constant<int, 0>());
   load_all();
   scales_at(cs);
 #pragma unroll
@@ -367,6 +369,7 @@ wide_block_kernel(const BlockArgs a) {
   //    longer to land, the reads less time.)
   using Paired = Order<FM, true>;
   using Rows = Order<FM, false>;
+  static_assert(4 + XB + 2 <= 19, "the scales' loads come before the handshake");
   constexpr int HS = 19, LW = HS + 1 + (NM - HS) * 3 / 4;
   auto kstep = [&](auto first_c, auto pending_c) {
     constexpr bool FIRST = decltype(first_c)::value, PENDING = decltype(pending_c)::value;
@@ -400,7 +403,7 @@ wide_block_kernel(const BlockArgs a) {
             if constexpr (i >= 4 && i - 4 < XB + 2) read_scale(i - 4);
             if constexpr (i == NM - 4) use_a(0);
             if constexpr (ROWB && i == NM - 3) use_b(0);
-            if constexpr (i == HS) handshake(c + 1);
+            if constexpr (i == HS) handshake(c + 1, std::integral_constant<int, XB + 2>());
             if constexpr (i >= HS) {
               // (rows that were done before it at the handshake)
               [&]<int... F>(std::integer_sequence<int, F...>) {

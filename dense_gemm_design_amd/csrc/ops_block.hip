@@ -419,9 +419,9 @@ int check(const gemm_block_desc *d) {
     if (d->scale_ldb < (d->block_b == GEMM_BLOCK_ROW ? d->N : (d->N + 127) / 128))
       return GEMM_ERR_INVALID_ARG;
   }
-  // offsets inside a tile of 256 rows stay under 31 bits, tile counts under 2^31
+  // offsets inside a tile of 256 rows (of A, B or C) stay under 31 bits, work-items under 2^32
   if (d->lda > (1 << 22) || d->ldb > (1 << 22)) return GEMM_ERR_UNSUPPORTED;
-  if (d->M > (1ll << 31) || d->N > (1ll << 31)) return GEMM_ERR_UNSUPPORTED;
+  if (d->M > (1ll << 31) || d->N > (1ll << 22)) return GEMM_ERR_UNSUPPORTED;
   if (((d->M + 127) / 128) * ((d->N + 127) / 128) > (1ll << 22)) return GEMM_ERR_UNSUPPORTED;
   return GEMM_OK;
 }

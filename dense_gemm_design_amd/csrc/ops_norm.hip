@@ -349,6 +349,7 @@ __global__ void __launch_bounds__(1024)
 }
 
 constexpr int kCUs = 256;
+constexpr int64_t kMost = 1 << 24;   // columns: the join's work-items stay under 2^32
 constexpr int64_t kLong = 1024 * 8 * 3, kGradLong = 512 * 8 * 4;   // the longest rows in registers
 
 // Workgroups of a backward pass: one a CU.  515 x 1111 fp32 takes 17.6 us on 64, 11.8 on 128, 9.8 on
@@ -435,6 +436,7 @@ extern "C" int gemm_layer_norm(const void *x, int dtype, int64_t rows, int64_t c
   using namespace dg;
   if (rows < 0 || cols <= 0 || !types_ok(dtype, wtype) || !stride_ok(rows, cols, stride))
     return GEMM_ERR_INVALID_ARG;
+  if (cols > kMost) return GEMM_ERR_UNSUPPORTED;
   if (rows == 0) return GEMM_OK;
   if (!x || !w || !y || !mean || !rstd) return GEMM_ERR_INVALID_ARG;
   if (!aligned(x, elem(dtype)) || !aligned(y, elem(dtype)) || !aligned(w, elem(wtype)) ||
@@ -463,6 +465,7 @@ extern "C" int gemm_layer_norm(const void *x, int dtype, int64_t rows, int64_t c
 
 extern "C" int gemm_layer_norm_backward_workspace(int64_t rows, int64_t cols, size_t *bytes) {
   if (rows < 0 || cols <= 0 || !bytes) return GEMM_ERR_INVALID_ARG;
+  if (cols > dg::kMost) return GEMM_ERR_UNSUPPORTED;
   *bytes = (size_t)dg::grad_groups(rows, cols) * 2 * (size_t)cols * sizeof(float);
   return GEMM_OK;
 }
@@ -476,6 +479,7 @@ extern "C" int gemm_layer_norm_backward(const void *dy, int64_t dstride, const v
   if (rows < 0 || cols <= 0 || !types_ok(dtype, wtype) || !stride_ok(rows, cols, stride) ||
       !stride_ok(rows, cols, dstride) || !w || !dw || !db)
     return GEMM_ERR_INVALID_ARG;
+  if (cols > kMost) return GEMM_ERR_UNSUPPORTED;
   if (rows > 0 && (!dy || !x || !mean || !rstd || !dx)) return GEMM_ERR_INVALID_ARG;
   if (!aligned(x, elem(dtype)) || !aligned(dy, elem(dtype)) || !aligned(dx, elem(dtype)) ||
       !aligned(w, elem(wtype)) || !aligned(dw, elem(wtype)) || !aligned(db, elem(wtype)) ||

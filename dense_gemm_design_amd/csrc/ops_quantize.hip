@@ -318,7 +318,7 @@ extern "C" int gemm_block_quantize(const void *x, int dtype, int64_t rows, int64
   if (codes_t && (pitch_t < rows || pitch_t % 16 || pitch_t >= rows + 16 ||
                   (rt > 1 && scale_pitch_t < (tile ? ct : cols))))
     return GEMM_ERR_INVALID_ARG;
-  if (rt > 0x7FFFFFFF / ct) return GEMM_ERR_UNSUPPORTED;
+  if (rt > 0xFFFFFF / ct) return GEMM_ERR_UNSUPPORTED;   // 2^32 work-items
   if (!aligned(x, dtype == GEMM_BF16 ? 2 : 4) || !aligned(codes, 16) || !aligned(codes_t, 16) ||
       !aligned(scales, 4) || !aligned(scales_t, 4))
     return GEMM_ERR_ALIGNMENT;

@@ -199,6 +199,26 @@ def test_c_abi_refusals():
     assert lib.gemm_grad_norm(None, 3, P, P, 1 << 40, None) == inv
 
 
+def test_c_abi_limits():
+    """Sizes whose offsets or launches would pass 32 bits are refused."""
+    lib = O.load()
+    n = ctypes.c_size_t()
+    uns = L.GEMM_ERR_UNSUPPORTED
+    d = dict(M=1, N=1, K=16, lda=16, ldb=16, scale_lda=1, scale_ldb=1, dtype_c=2, dtype_source=2)
+    for kw, want in ((dict(N=1 << 22), 0), (dict(N=(1 << 22) + 1), uns), (dict(M=(1 << 31) + 1), uns),
+                     (dict(lda=(1 << 22) + 16), uns), (dict(M=1 << 30, N=1 << 21), uns)):
+        assert lib.gemm_block_workspace(O.GemmBlockDesc(**{**d, **kw}), ctypes.byref(n)) == want, kw
+    assert lib.gemm_layer_norm_backward_workspace(1, 1 << 24, ctypes.byref(n)) == 0
+    assert lib.gemm_layer_norm_backward_workspace(1, (1 << 24) + 1, ctypes.byref(n)) == uns
+    c = (1 << 24) + 1
+    assert lib.gemm_layer_norm(P, 2, 1, c, c, P, P, 2, 1e-5, P, P, P, None) == uns
+    assert lib.gemm_layer_norm_backward(P, c, P, c, 2, 1, c, P, 2, P, P, P, P, P, P, 1 << 50,
+                                        None) == uns
+    big = 1 << 20
+    assert lib.gemm_block_quantize(P, 2, big * 128, big * 128, big * 128, 0, 0, P, big * 128, P,
+                                   big * 128, None, 0, None, 0, None) == uns
+
+
 def test_workspaces_cover_their_sums():
     lib = O.load()
     n = ctypes.c_size_t()

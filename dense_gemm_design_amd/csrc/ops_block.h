@@ -12,13 +12,13 @@ struct BlockArgs {
   char *C;
   const float *bias;
   const char *source;
-  float *partials;          // splits > 1: [split][M][N]
+  float *partials;          // splits > 1: [split][M][N] of few rows, [split][tile][128][128] of tiles
   int64_t M, N;
   int64_t lda, ldb, lsa, lsb;
   int32_t kbytes;           // K rounded up to 16: what is read of a row
   int32_t kb;               // blocks of 128 along K
   int32_t mt, nt;           // tiles
-  int32_t splits;
+  int32_t splits, whole;    // pieces of K; the tiles in front that are not cut
   int32_t out_bf16, src_bf16;
   int32_t plain_rows;       // no source, and rows of C in whole, aligned 16 bytes
 };

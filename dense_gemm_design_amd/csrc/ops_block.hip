@@ -22,35 +22,58 @@
 namespace dg {
 namespace {
 
+constexpr int kTile = 128;   // rows and columns of the smaller tiles
+
 // ---- tiles through LDS ------------------------------------------------------------------------
 
-// WGM x WGN waves own a BM x BN tile of C; a ring of two stages in LDS holds the k-block that is
-// multiplied and the next one on its way (loads that write LDS directly, rows swizzled in 16-byte
-// chunks as in the plain product's kernels).  The scales of a stage's block travel with it.
+// Where tile t of the order lies: strips of eight rows of tiles, walked down first.
+__device__ __forceinline__ void tile_corner(const BlockArgs &a, int32_t t, int bm, int bn,
+                                            int64_t &m0, int64_t &n0) {
+  const int32_t strip = t / (8 * a.nt), in = t % (8 * a.nt);
+  const int32_t high = a.mt - strip * 8 < 8 ? a.mt - strip * 8 : 8;
+  m0 = (int64_t)(strip * 8 + in % high) * bm;
+  n0 = (int64_t)(in / high) * bn;
+}
+// The place of workgroup i of n, so that those of one XCD (i mod 8) are neighbours.
+__device__ __forceinline__ int32_t place(int32_t i, int32_t n) {
+  const int32_t per = n / 8, more = n % 8, x = i % 8;
+  return x * per + (x < more ? x : more) + i / 8;
+}
+
+// KG groups of WGM x WGN waves own a BM x BN tile of C, each for every KG-th k-block; their sums meet
+// in LDS.  A ring of two stages a group in LDS holds the k-block that is multiplied and the next one
+// on its way (loads that write LDS directly, rows swizzled in 16-byte chunks as in the plain product's
+// kernels).  The scales of a stage's block travel with it.
+//
+// The first a.whole tiles have a workgroup each; the k-blocks of the others are cut into a.splits
+// pieces, whose sums join_tiles_kernel adds.
 enum { MODE_FMA, MODE_POW2, MODE_EXACT };
-template <int BM, int BN, int WGM, int WGN, bool ROWB, int MODE>
-__global__ void __launch_bounds__(WGM *WGN * 64, 2) block_kernel(const BlockArgs a) {
+template <int BM, int BN, int WGM, int WGN, int KG, bool ROWB, int MODE>
+__global__ void __launch_bounds__(KG *WGM *WGN * 64, 2) block_kernel(const BlockArgs a) {
   constexpr int NW = WGM * WGN, WM = BM / WGM, WN = BN / WGN, FM = WM / 16, FN = WN / 16;
   constexpr int LA = BM / 8 / NW, LB = BN / 8 / NW;   // 1 KiB loads (8 rows) a wave and stage
   constexpr int SCALES = (BM + BN) * 4, STAGE = (BM + BN) * 128 + SCALES;
   static_assert(BM % 64 == 0 && BN % 64 == 0 && (BM + BN) / 64 == NW, "one scale load a wave");
-  __shared__ __align__(1024) char smem_[2 * STAGE];
-  lds_t *const smem = (lds_t *)smem_;
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
+  __shared__ __align__(1024) char smem_[KG * 2 * STAGE];
+  const int wave_ = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
+  const int group = wave_ / NW, wave = wave_ % NW;
+  lds_t *const smem = (lds_t *)smem_ + group * 2 * STAGE;
 
-  // the tiles of one XCD are neighbours: eight rows of tiles, walked down first
-  const int32_t tiles = a.mt * a.nt;
-  const int32_t split = blockIdx.x / (uint32_t)tiles;
-  int32_t t = blockIdx.x % (uint32_t)tiles;
-  {
-    const int32_t per = tiles / 8, more = tiles % 8, x = t % 8, i = t / 8;
-    t = x * per + (x < more ? x : more) + i;
+  const int32_t i = blockIdx.x, cut = a.mt * a.nt - a.whole;   // tiles whose K is cut
+  int32_t t, piece = -1, kb0 = 0, kb1 = a.kb;   // piece: of the partial sums
+  if (i < a.whole) {
+    t = place(i, a.whole);
+  } else {
+    const int32_t split = (i - a.whole) / cut, at = place((i - a.whole) % cut, cut);
+    t = a.whole + at;
+    if (a.splits > 1) {
+      piece = split * cut + at;
+      kb0 = (int32_t)((int64_t)a.kb * split / a.splits);
+      kb1 = (int32_t)((int64_t)a.kb * (split + 1) / a.splits);
+    }
   }
-  const int32_t strip = t / (8 * a.nt), in = t % (8 * a.nt);
-  const int32_t high = a.mt - strip * 8 < 8 ? a.mt - strip * 8 : 8;
-  const int64_t m0 = (int64_t)(strip * 8 + in % high) * BM, n0 = (int64_t)(in / high) * BN;
-  const int32_t kb0 = (int32_t)((int64_t)a.kb * split / a.splits);
-  const int32_t kb1 = (int32_t)((int64_t)a.kb * (split + 1) / a.splits);
+  int64_t m0, n0;
+  tile_corner(a, t, BM, BN, m0, n0);
 
   // producer
   const int32_t rows_a = (int32_t)(a.M - m0 < BM ? a.M - m0 : BM);
@@ -108,14 +131,15 @@ __global__ void __launch_bounds__(WGM *WGN * 64, 2) block_kernel(const BlockArgs
   // a wave wholly past the edge only loads
   const bool inside = m0 + wm * WM < a.M && n0 + wn * WN < a.N;
 
-  if (kb0 < kb1) load_stage(kb0, 0);
-  for (int32_t kb = kb0; kb < kb1; ++kb) {
-    const int s = (kb - kb0) & 1;
+  if (kb0 + group < kb1) load_stage(kb0 + group, 0);
+  int s = 1;
+  for (int32_t kb = kb0 + group; kb < kb1 + group; kb += KG) {   // as often in every group
+    s ^= 1;
     // this wave's loads of the stage have landed and its reads of the other stage are done; after
     // the barrier that holds for every wave
     asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
-    if (kb + 1 < kb1) load_stage(kb + 1, s ^ 1);
-    if (!inside) continue;
+    if (kb + KG < kb1) load_stage(kb + KG, s ^ 1);
+    if (!inside || kb >= kb1) continue;
     const lds_t *const st = smem + s * STAGE;
     typedef const float __attribute__((address_space(3))) *fp;
     typedef const f32x4 __attribute__((address_space(3))) *f4p;
@@ -178,23 +202,67 @@ __global__ void __launch_bounds__(WGM *WGN * 64, 2) block_kernel(const BlockArgs
     }
   }
 
+  // each group gives away the sums of the rows of blocks that the other one writes
+  constexpr int OWN = FM / KG;
+  static_assert(KG == 1 || (KG == 2 && OWN * KG == FM && NW * OWN * FN * 1024 <= 2 * STAGE), "");
+  if constexpr (KG == 2) {
+    typedef f32x4 __attribute__((address_space(3))) *f4p;
+    lds_t *const area = (lds_t *)smem_ + wave * (OWN * FN * 1024) + lane * 16;
+    asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");   // all stages are read
 #pragma unroll
-  for (int f = 0; f < FM; ++f) {
-    const int64_t m = m0 + wm * WM + f * 16 + r16;
-    if (m >= a.M) continue;
+    for (int f = 0; f < OWN; ++f)
+#pragma unroll
+      for (int g = 0; g < FN; ++g)
+        *(f4p)(area + (group ^ 1) * 2 * STAGE + (f * FN + g) * 1024) =
+            group ? acc[f][g] : acc[f + OWN][g];
+    asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+#pragma unroll
+    for (int f = 0; f < OWN; ++f)
+#pragma unroll
+      for (int g = 0; g < FN; ++g)
+        acc[f][g] = (group ? acc[f + OWN][g] : acc[f][g]) +
+                    *(f4p)(area + group * 2 * STAGE + (f * FN + g) * 1024);
+  }
+#pragma unroll
+  for (int f = 0; f < OWN; ++f) {
+    const int ml = wm * WM + (group * OWN + f) * 16 + r16;
+    if (m0 + ml >= a.M) continue;
 #pragma unroll
     for (int g = 0; g < FN; ++g) {
-      const int64_t n = n0 + wn * WN + g * 16 + g4 * 4;
-      if (n >= a.N) continue;
-      if (a.splits > 1)
-        partial_four(a, split, m, n, acc[f][g]);
+      const int nl = wn * WN + g * 16 + g4 * 4;
+      if (n0 + nl >= a.N) continue;
+      if (piece >= 0)
+        *(f32x4 *)(a.partials + (int64_t)piece * (BM * BN) + ml * BN + nl) = acc[f][g];
       else
-        store_four(a, m, n, acc[f][g]);
+        store_four(a, m0 + ml, n0 + nl, acc[f][g]);
     }
   }
 }
 
-// Adds the splits' sums in order, then the epilogue.
+// Adds the pieces of the tiles whose K is cut, in order, then the epilogue.  Eight rows of a tile a
+// workgroup.
+__global__ void __launch_bounds__(256) join_tiles_kernel(const BlockArgs a) {
+  constexpr int B = kTile;
+  const int32_t cut = a.mt * a.nt - a.whole, at = blockIdx.x / (B / 8);
+  const int ml = blockIdx.x % (B / 8) * 8 + threadIdx.x / 32, nl = threadIdx.x % 32 * 4;
+  int64_t m0, n0;
+  tile_corner(a, a.whole + at, B, B, m0, n0);
+  if (m0 + ml >= a.M || n0 + nl >= a.N) return;
+  f32x4 v = {0, 0, 0, 0};
+  for (int s = 0; s < a.splits; s += 8) {
+    f32x4 q[8];   // loads in flight together
+#pragma unroll
+    for (int u = 0; u < 8; ++u)
+      q[u] = s + u < a.splits ? *(const f32x4 *)(a.partials + (int64_t)((s + u) * cut + at) * (B * B) +
+                                                 ml * B + nl)
+                              : f32x4{0, 0, 0, 0};
+#pragma unroll
+    for (int u = 0; u < 8; ++u) v += q[u];
+  }
+  store_four(a, m0 + ml, n0 + nl, v);
+}
+
+// Adds the splits' sums of few rows in order, then the epilogue.
 __global__ void __launch_bounds__(256) join_kernel(const BlockArgs a) {
   const int64_t per_row = (a.N + 3) / 4, all = a.M * per_row;
   for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < all; i += (int64_t)gridDim.x * 256) {
@@ -331,10 +399,10 @@ __global__ void __launch_bounds__(512) few_kernel(const BlockArgs a) {
 
 constexpr int kCUs = 256;
 
-enum { PLAN_FEW, PLAN_128, PLAN_256, PLAN_WIDE };
+enum { PLAN_FEW, PLAN_128, PLAN_CUT, PLAN_256, PLAN_WIDE };
 struct BlockPlan {
   int kind, splits;
-  int32_t mt, nt;
+  int32_t mt, nt, whole;   // whole: the tiles whose K is not cut
 };
 
 int few_columns(const gemm_block_desc &d) { return d.M > 16 && d.N > 16 * kCUs ? 32 : 16; }
@@ -349,7 +417,7 @@ BlockPlan plan_of(const gemm_block_desc &d) {
     const int64_t nt = (d.N + cols - 1) / cols;
     int64_t splits = nt < 128 ? 256 / nt : 1;
     if (splits > kb / 16) splits = kb / 16;
-    return {PLAN_FEW, splits > 1 ? (int)splits : 1, 1, (int32_t)nt};
+    return {PLAN_FEW, splits > 1 ? (int)splits : 1, 1, (int32_t)nt, 0};
   }
   if (d.dtype_c == GEMM_BF16 && kb) {
     // Tiles of 256 x 256 (wide with powers of two, eight waves otherwise) or, for fp32 scales of 128 x
@@ -363,40 +431,57 @@ BlockPlan plan_of(const gemm_block_desc &d) {
     const int rows = narrow ? wide_rows(false) : 256;
     const int64_t mt = (d.M + rows - 1) / rows, nt = (d.N + 255) / 256;
     if (mt * nt >= kCUs)
-      return {d.pow2 || narrow ? PLAN_WIDE : PLAN_256, 1, (int32_t)mt, (int32_t)nt};
+      return {d.pow2 || narrow ? PLAN_WIDE : PLAN_256, 1, (int32_t)mt, (int32_t)nt, (int32_t)(mt * nt)};
   }
-  // Tiles of 128 x 128 (an fp32 C's codes as bf16 leave no registers for larger sub-tiles), two
-  // workgroups a CU, and K cut so that the estimate below is least.  A k-block takes a CU c1 us with
-  // one workgroup and c2 with two: 1.29 and 2.1 measured with an fp32 C, 1.0 and 1.38 with bf16.  What
-  // the pieces leave costs 8 bytes an element and piece to write and read, and a launch.  (us on one,
-  // two, three, four, six pieces: 1000 x 4104 x 8201 fp32 136, 118, 107, 105, 107; 256 x 4096 x 4096
-  // bf16 28, 23, 20, 19, 21; 64 x 16384 x 16384 bf16 108, 68, 57, 52, 64.)
-  const int64_t mt = (d.M + 127) / 128, nt = (d.N + 127) / 128, t = mt * nt;
+  // Tiles of 128 x 128 (an fp32 C's codes as bf16 leave no registers for larger sub-tiles).  Either
+  // PLAN_128, two workgroups a CU, a tile each: a k-block takes c1 us for one of them alone, c2 for two.
+  // Or PLAN_CUT, one of twice the waves a CU, which takes two k-blocks in c us, and a round of tiles
+  // 1.5 us more, in which it only writes: as many tiles as fill rounds of all CUs are taken whole, and K
+  // is cut for the rest, which costs 8 bytes an element and piece to write and read, and a launch.  What
+  // is less by this estimate.  (us on PLAN_128 and PLAN_CUT, fp32: 4096 x 14336 x 4096 481, 533; 2048 x
+  // 4096 x 8192 136, 143; 2048 x 2048 x 8192 86, 78; 1000 x 4104 x 8201 136, 93.  bf16, fp32 scales: 80,
+  // 89 and 64, 49 for the two in the middle; powers of two: 69, 78 and 52, 43.)
+  const int64_t mt = (d.M + kTile - 1) / kTile, nt = (d.N + kTile - 1) / kTile;
+  const int64_t t = mt * nt, rest = t % kCUs;
   const bool f32 = d.dtype_c == GEMM_F32;
-  const double c1 = f32 ? 1.29 : 1.0, c2 = f32 ? 2.1 : 1.38;
+  const double c1 = f32 ? 1.3 : d.pow2 ? 0.75 : 0.9, c2 = f32 ? 2.1 : d.pow2 ? 1.05 : 1.27;
+  const double c = f32 ? 2.33 : d.pow2 ? 1.22 : 1.45;
+  const int64_t last = t % (2 * kCUs);
+  const double pairs =
+      (double)kb * ((double)(t / (2 * kCUs)) * c2 + (last > kCUs ? c2 : last ? c1 : 0.0));
   int splits = 1;
   double least = 0.0;
-  for (int s = 1; s <= 64 && (s == 1 || (s * 2 <= kb && t * s <= 8 * kCUs)); ++s) {
-    const double groups = (double)t * s, blocks = (double)((kb + s - 1) / s);
-    double us = groups <= kCUs ? blocks * c1
-                : groups <= 2 * kCUs ? blocks * c2
-                                     : (groups / (2 * kCUs) + 0.5) * blocks * c2;
-    if (s > 1) us += 3.0 + (double)d.M * (double)d.N * 8e-6 / 8.0 * s;
+  for (int s = 1; s <= 64 && (s == 1 || (rest && s * 2 <= kb && rest * s <= 8 * kCUs)); ++s) {
+    const int64_t steps = ((kb + s - 1) / s + 1) / 2, rounds = (rest * s + kCUs - 1) / kCUs;
+    double us = (double)rounds * ((double)steps * c + 1.5);
+    if (s > 1) us += 3.0 + (double)(rest * s) * (kTile * kTile) * 1e-6;
     if (s == 1 || us < least) {
       least = us;
       splits = s;
     }
   }
-  return {PLAN_128, splits, (int32_t)mt, (int32_t)nt};
+  if (pairs <= (double)(t / kCUs) * ((double)((kb + 1) / 2) * c + 1.5) + least)
+    return {PLAN_128, 1, (int32_t)mt, (int32_t)nt, (int32_t)t};
+  return {PLAN_CUT, splits, (int32_t)mt, (int32_t)nt, (int32_t)(t - rest)};
 }
 
-template <int BM, int BN, int WGM, int WGN, int MODE>
+template <int BM, int BN, int WGM, int WGN, int KG, int MODE>
 void launch_tiles(const BlockArgs &a, bool rowb, hipStream_t s) {
-  const dim3 grid((uint32_t)((int64_t)a.mt * a.nt * a.splits)), block(WGM * WGN * 64);
+  const dim3 grid((uint32_t)(a.whole + (a.mt * a.nt - a.whole) * a.splits)),
+      block(KG * WGM * WGN * 64);
   if (rowb)
-    hipLaunchKernelGGL((block_kernel<BM, BN, WGM, WGN, true, MODE>), grid, block, 0, s, a);
+    hipLaunchKernelGGL((block_kernel<BM, BN, WGM, WGN, KG, true, MODE>), grid, block, 0, s, a);
   else
-    hipLaunchKernelGGL((block_kernel<BM, BN, WGM, WGN, false, MODE>), grid, block, 0, s, a);
+    hipLaunchKernelGGL((block_kernel<BM, BN, WGM, WGN, KG, false, MODE>), grid, block, 0, s, a);
+}
+template <int KG>
+void launch_small(const BlockArgs &a, bool rowb, const gemm_block_desc &d, hipStream_t s) {
+  if (d.dtype_c == GEMM_F32)
+    launch_tiles<kTile, kTile, 2, 2, KG, MODE_EXACT>(a, rowb, s);
+  else if (d.pow2)
+    launch_tiles<kTile, kTile, 2, 2, KG, MODE_POW2>(a, rowb, s);
+  else
+    launch_tiles<kTile, kTile, 2, 2, KG, MODE_FMA>(a, rowb, s);
 }
 template <int FM, int GN>
 void launch_few(const BlockArgs &a, bool rowb, hipStream_t s) {
@@ -436,7 +521,10 @@ extern "C" int gemm_block_workspace(const gemm_block_desc *d, size_t *bytes) {
   *bytes = 0;
   if (d->M == 0 || d->N == 0) return GEMM_OK;
   const dg::BlockPlan p = dg::plan_of(*d);
-  if (p.splits > 1) *bytes = (size_t)p.splits * (size_t)d->M * (size_t)d->N * sizeof(float);
+  if (p.splits > 1)
+    *bytes = (size_t)p.splits * sizeof(float) *
+             (p.kind == dg::PLAN_FEW ? (size_t)d->M * (size_t)d->N
+                                     : (size_t)(p.mt * p.nt - p.whole) * (dg::kTile * dg::kTile));
   return GEMM_OK;
 }
 
@@ -478,6 +566,7 @@ extern "C" int gemm_block_run(const gemm_block_desc *d, const void *A, const flo
   a.mt = p.mt;
   a.nt = p.nt;
   a.splits = p.splits;
+  a.whole = p.whole;
   a.out_bf16 = d->dtype_c == GEMM_BF16;
   a.src_bf16 = d->dtype_source == GEMM_BF16;
   a.plain_rows = !source && (d->N * (a.out_bf16 ? 2 : 4)) % 16 == 0 && !((uintptr_t)C & 15);
@@ -491,18 +580,20 @@ extern "C" int gemm_block_run(const gemm_block_desc *d, const void *A, const flo
     else
       launch_few<2, 2>(a, rowb, s);
   } else if (p.kind == PLAN_256) {
-    launch_tiles<256, 256, 2, 4, MODE_FMA>(a, rowb, s);
+    launch_tiles<256, 256, 2, 4, 1, MODE_FMA>(a, rowb, s);
   } else if (p.kind == PLAN_WIDE) {
     if (launch_block_wide(a, rowb, d->pow2 != 0, s) != hipSuccess) return GEMM_ERR_HIP;
-  } else if (d->dtype_c == GEMM_F32) {
-    launch_tiles<128, 128, 2, 2, MODE_EXACT>(a, rowb, s);
-  } else if (d->pow2) {
-    launch_tiles<128, 128, 2, 2, MODE_POW2>(a, rowb, s);
+  } else if (p.kind == PLAN_128) {
+    launch_small<1>(a, rowb, *d, s);
   } else {
-    launch_tiles<128, 128, 2, 2, MODE_FMA>(a, rowb, s);
+    launch_small<2>(a, rowb, *d, s);
   }
   if (hipGetLastError() != hipSuccess) return GEMM_ERR_HIP;
-  if (p.splits > 1) {
+  if (p.splits > 1 && p.kind != PLAN_FEW) {
+    hipLaunchKernelGGL(join_tiles_kernel, dim3((uint32_t)((p.mt * p.nt - p.whole) * (kTile / 8))),
+                       dim3(256), 0, s, a);
+    if (hipGetLastError() != hipSuccess) return GEMM_ERR_HIP;
+  } else if (p.splits > 1) {
     const int64_t need_wg = (d->M * ((d->N + 3) / 4) + 255) / 256;
     hipLaunchKernelGGL(join_kernel, dim3((uint32_t)(need_wg < 8 * kCUs ? need_wg : 8 * kCUs)),
                        dim3(256), 0, s, a);

@@ -246,6 +246,33 @@ def test_product_of_large_tiles(dev, M, N, K, block, pow2):
         assert bool((held[:at] == 5).all()) and bool((held[at + M * N:] == 5).all())
 
 
+@pytest.mark.parametrize("pow2", [False, True], ids=["any", "pow2"])
+@pytest.mark.parametrize("block", ["row", "tile"])
+@pytest.mark.parametrize("M,N,K", [(2171, 2045, 4300), (140, 139, 16000), (1300, 1300, 1100),
+                                   (33, 4300, 3700)])
+def test_product_of_cut_tiles(dev, M, N, K, block, pow2):
+    """Few tiles of much K, and some over what fills the chip: pieces of odd and even length, edges in
+    them, and all that is added behind them; memory around C stays as it was."""
+    print(f"product {M}x{N}x{K} b {block} pow2={pow2}", flush=True)
+    g = gen(M + N + K)
+    a, av = operand(g, dev, M, K, "row", pow2)
+    b, bv = operand(g, dev, N, K, block, pow2)
+    av, bv = av.to(dev), bv.to(dev)
+    bias, src = randn(g, N).to(dev), randn(g, M, N).to(BF16).to(dev)
+    extras = [bias.double(), src.double()]
+    want = torch.mm(av, bv.t().contiguous()) + extras[0] + extras[1]
+    for dt in (BF16, F32):
+        whole = torch.full((M + 2, N), 7.0, dtype=dt, device=dev)
+        dg.block_gemm(a, b, bias_col=bias, source=src, out=whole[1:-1])
+        bound = product_bound(av, bv, K, want, dt, extras)
+        bad = ~((whole[1:-1].double() - want).abs() <= bound)
+        assert not bool(bad.any()), (dt, int(bad.sum()), bad.nonzero()[0].tolist())
+        assert bool((whole[0] == 7).all()) and bool((whole[-1] == 7).all())
+        again = torch.empty(M, N, dtype=dt, device=dev)
+        dg.block_gemm(a, b, bias_col=bias, source=src, out=again)
+        assert torch.equal(again, whole[1:-1]), "sums in another order"
+
+
 def test_product_adds_into_its_source(dev):
     g = gen(11)
     for M, N, K in ((20, 70, 300), (200, 70, 300), (64, 130, 9000)):

@@ -9,11 +9,13 @@
 // many rows: w and b, and the sums of dw and db for a thread's columns, stay in registers too, and
 // the next row's loads are in flight while the present one is summed.  A workgroup's dw and db go
 // to the workspace as one row of partial sums; a second kernel adds those in a fixed order, so
-// results do not change from run to run.  All sums are in fp32.
+// results do not change from run to run.  Few rows take one launch.  All sums are in fp32.
 //
 // Bound by memory: forward 2, backward 3 elements a column.
 #include "../../include/gemm_ops.h"
 #include "ops_common.h"
+
+#include <type_traits>
 
 namespace dg {
 namespace {
@@ -24,6 +26,7 @@ struct NormArgs {
   float *mean, *rstd;   // written forward, read backward
   float *partials;      // backward: one row of 2 x cols sums per workgroup
   int64_t rows, cols, stride, dstride;
+  int64_t row_groups;   // norm_grad_few_kernel
   float eps;
 };
 
@@ -260,6 +263,98 @@ __global__ void __launch_bounds__(Geo<WAVES>::THREADS) norm_grad_kernel(const No
   }
 }
 
+// Few rows, where launches and trips to memory count and not bytes: one launch, whose first a.row_groups
+// workgroups take the rows' dx, and the others the dw and db of 16 columns each, from their own reading of
+// x and dy (out of the caches for the most part).  128 x 1000 fp32 3.2 us (6.5 with partial sums and a
+// launch to join them), 515 x 1111 7.0 (10.1), 515 x 4096 11.1 (12.7).  With 8 columns a workgroup, which
+// reads half as much of a line: 3.1, 6.7, 15.6.
+constexpr int kFewCols = 16;
+template <class T, class W, int WAVES, int NV>
+__global__ void __launch_bounds__(256) norm_grad_few_kernel(const NormArgs a, W *dw, W *db) {
+  static_assert(Geo<WAVES>::THREADS == 256, "");
+  constexpr int ROWS = Geo<WAVES>::ROWS, SPAN = WAVES * 64;
+  if ((int64_t)blockIdx.x >= a.row_groups) {
+    constexpr int COLS = kFewCols, LANES = 256 / COLS;   // LANES threads take every LANES-th row
+    __shared__ float part[2][LANES][COLS + 1];
+    const int c = threadIdx.x % COLS, r0 = threadIdx.x / COLS;
+    const int64_t col = ((int64_t)blockIdx.x - a.row_groups) * COLS + c;
+    float sw = 0.0f, sb = 0.0f;
+    const T *const x = (const T *)a.x + (col < a.cols ? col : 0);
+    const T *const dy = (const T *)a.dy + (col < a.cols ? col : 0);
+    // FLIGHT rows, loaded together; a row past the last is read as row 0 and counts nothing
+    auto take = [&](int64_t r, auto flight_c) {
+      constexpr int FLIGHT = decltype(flight_c)::value;
+      float xv[FLIGHT], gv[FLIGHT], mean[FLIGHT], rstd[FLIGHT];
+#pragma unroll
+      for (int u = 0; u < FLIGHT; ++u) {
+        const int64_t at = r + LANES * u < a.rows ? r + LANES * u : 0;
+        xv[u] = load1(x + at * a.stride);
+        gv[u] = load1(dy + at * a.dstride);
+        mean[u] = a.mean[at];
+        rstd[u] = a.rstd[at];
+      }
+#pragma unroll
+      for (int u = 0; u < FLIGHT; ++u)
+        if (r + LANES * u < a.rows) {
+          sw = fmaf(gv[u], (xv[u] - mean[u]) * rstd[u], sw);
+          sb += gv[u];
+        }
+    };
+    int64_t r = 0;
+    for (; r + LANES * 4 < a.rows; r += LANES * 16) take(r + r0, std::integral_constant<int, 16>());
+    for (; r < a.rows; r += LANES * 4) take(r + r0, std::integral_constant<int, 4>());
+    part[0][r0][c] = sw;
+    part[1][r0][c] = sb;
+    __syncthreads();
+    if (r0 < 2 && col < a.cols) {
+      float s = 0.0f;
+#pragma unroll
+      for (int i = 0; i < LANES; ++i) s += part[r0][i][c];
+      store1((r0 ? db : dw) + col, s);
+    }
+    return;
+  }
+  __shared__ float red[WAVES][2];
+  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+  const int t = ROWS == 1 ? threadIdx.x : lane;
+  const int64_t row = (int64_t)blockIdx.x * ROWS + (ROWS == 1 ? 0 : wave);
+  if (row >= a.rows) return;   // a whole wave, and with one row a workgroup none
+  Vec8<T> x[NV], g[NV];
+  Vec8<W> w[NV];
+#pragma unroll
+  for (int v = 0; v < NV; ++v) {
+    const int64_t e = (int64_t)(v * SPAN + t) * 8;
+    load8(x[v], (const T *)a.x + row * a.stride + e, a.cols - e);
+    load8(g[v], (const T *)a.dy + row * a.dstride + e, a.cols - e);
+    load8(w[v], (const W *)a.w + e, a.cols - e);
+  }
+  const float mean = a.mean[row], rstd = a.rstd[row], inv_n = 1.0f / (float)a.cols;
+  float s[2] = {0.0f, 0.0f};
+#pragma unroll
+  for (int v = 0; v < NV; ++v) {
+    const int64_t left = a.cols - (int64_t)(v * SPAN + t) * 8;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float h = i < left ? (x[v].at(i) - mean) * rstd : 0.0f, gw = g[v].at(i) * w[v].at(i);
+      s[0] += gw;
+      s[1] = fmaf(gw, h, s[1]);
+    }
+  }
+  group_sum<WAVES, 2>(s, red, wave, lane);
+  const float mg = s[0] * inv_n, mgh = s[1] * inv_n;
+#pragma unroll
+  for (int v = 0; v < NV; ++v) {
+    const int64_t e = (int64_t)(v * SPAN + t) * 8;
+    float dx[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float h = (x[v].at(i) - mean) * rstd;
+      dx[i] = rstd * (fmaf(g[v].at(i), w[v].at(i), -mg) - h * mgh);
+    }
+    store8((T *)a.y + row * a.cols + e, dx, a.cols - e);
+  }
+}
+
 // Long rows: two passes over each; a workgroup's sums of dw and db grow in its own row of the
 // workspace (each element is read and written by one thread only).
 template <class T, class W>
@@ -360,6 +455,13 @@ int grad_groups(int64_t rows, int64_t cols) {
   return (int)(need < kCUs ? need : kCUs);
 }
 
+// One launch for dx, dw and db, up to two trips of 16 rows and one of 4 a thread: 1024 rows take 10.1 us
+// at 1000 columns and 24.7 at 4096, and 9.0 and 15.2 the other way.  dx written over x or dy would
+// change what the columns' workgroups read.
+bool few_rows(const NormArgs &a) {
+  return a.rows > 0 && a.rows <= 256 / kFewCols * 36 && a.cols <= 4096 && a.y != a.x && a.y != a.dy;
+}
+
 // How many waves hold a row, and as how many vectors of eight a thread: one wave up to 1024 columns
 // (no barrier), then few enough vectors that the next row's loads find registers beside this one's.
 #define DG_NORM_SHAPES(KERNEL, cols)          \
@@ -403,6 +505,22 @@ void launch_norm(const NormArgs &a, hipStream_t s) {
 template <class T, class W>
 void launch_norm_grad(const NormArgs &a, W *dw, W *db, hipStream_t s) {
   const int grid = grad_groups(a.rows, a.cols);
+  if (few_rows(a)) {
+    NormArgs f = a;
+#define DG_FEW(WV, NV)                                                                           \
+  do {                                                                                           \
+    f.row_groups = (a.rows + Geo<WV>::ROWS - 1) / Geo<WV>::ROWS;                                 \
+    hipLaunchKernelGGL((norm_grad_few_kernel<T, W, WV, NV>),                                     \
+                       dim3((uint32_t)(f.row_groups + (a.cols + kFewCols - 1) / kFewCols)), \
+                       dim3(256), 0, s, f, dw, db);                                                                  \
+  } while (0)
+    if (a.cols <= 512) DG_FEW(1, 1);
+    else if (a.cols <= 1024) DG_FEW(1, 2);
+    else if (a.cols <= 2048) DG_FEW(4, 1);
+    else DG_FEW(4, 2);
+#undef DG_FEW
+    return;
+  }
   if (grid) {
     if (a.cols > kGradLong) {
       hipLaunchKernelGGL((norm_grad_long_kernel<T, W>), dim3(grid), dim3(1024), 0, s, a);

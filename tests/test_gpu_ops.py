@@ -1,9 +1,12 @@
 """The operators around the product against their plain forms in 64 bits."""
+import ctypes
+
 import pytest
 
 torch = pytest.importorskip("torch")
 
 import dense_gemm_design_amd as dg  # noqa: E402
+from dense_gemm_design_amd import ops as O  # noqa: E402
 import ops_ref as R  # noqa: E402
 
 pytestmark = pytest.mark.gpu
@@ -400,6 +403,48 @@ def test_layer_norm_backward(dev, rows, cols, types):
     x, w, _ = norm_inputs(g, dev, rows, cols, *types)
     dy = (0.1 * randn(g, rows, cols)).to(types[0]).to(dev)
     check_norm_grad(dy, x, w, f"{rows}x{cols}")
+
+
+@pytest.mark.parametrize("types", [(BF16, F32), (BF16, BF16), (F32, F32)],
+                         ids=["bf16-f32", "bf16-bf16", "f32-f32"])
+@pytest.mark.parametrize("rows,cols", [(15, 17), (17, 15), (64, 500), (65, 520), (255, 2050), (257, 33),
+                                       (515, 1111), (576, 2048), (577, 2048), (575, 1025), (580, 900),
+                                       (600, 3000), (576, 4097)])
+def test_layer_norm_backward_of_few_rows(dev, rows, cols, types):
+    print(f"layer norm backward {rows}x{cols} {types}", flush=True)
+    g = gen(rows + 2 * cols)
+    x, w, _ = norm_inputs(g, dev, rows, cols, *types)
+    dy = randn(g, rows, cols).to(types[0]).to(dev)
+    check_norm_grad(dy, x, w, f"{rows}x{cols}")
+    if rows <= 100:
+        wide = randn(g, rows, 2 * cols + 3).to(types[0]).to(dev)
+        check_norm_grad(dy[:1].expand(rows, cols), wide[:, 1:cols + 1], w, f"{rows}x{cols} strided")
+
+
+def test_layer_norm_backward_over_its_inputs(dev):
+    """dx may be written over dy or x through the C ABI."""
+    lib = O.load()
+    g = gen(41)
+    for rows, cols in ((40, 300), (300, 1500)):
+        x, w, _ = norm_inputs(g, dev, rows, cols, F32, F32)
+        dy = randn(g, rows, cols).to(dev)
+        _, mean, rstd = dg.layer_norm(x, w, None)
+        want = R.norm_grad(*(t.cpu() for t in (dy, x, w, mean, rstd)))
+        bounds = grad_bounds(dy, x, w, mean, rstd)
+        n = ctypes.c_size_t()
+        assert lib.gemm_layer_norm_backward_workspace(rows, cols, ctypes.byref(n)) == 0
+        work = torch.empty(n.value, dtype=torch.uint8, device=dev)
+        for over in ("dy", "x"):
+            d, v = dy.clone(), x.clone()
+            dx = d if over == "dy" else v
+            dw, db = torch.empty(cols, device=dev), torch.empty(cols, device=dev)
+            st = lib.gemm_layer_norm_backward(
+                d.data_ptr(), cols, v.data_ptr(), cols, 2, rows, cols, w.data_ptr(), 2,
+                mean.data_ptr(), rstd.data_ptr(), dx.data_ptr(), dw.data_ptr(), db.data_ptr(),
+                work.data_ptr(), n.value, torch.cuda.current_stream().cuda_stream)
+            assert st == 0
+            for o, t, e, name in zip((dx, dw, db), want, bounds, ("dx", "dw", "db")):
+                R.within(o, t, e + (t.abs() + e) * R.HALF[F32], f"over {over} {name}")
 
 
 def test_layer_norm_strided_rows(dev):

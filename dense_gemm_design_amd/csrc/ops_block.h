@@ -63,6 +63,54 @@ __device__ __forceinline__ void store_four(const BlockArgs &a, int64_t m, int64_
       ((float *)a.C)[at + i] = z;
   }
 }
+
+// The same in three steps, for kernels whose threads have many outputs: the extras are loaded for several
+// of them before the first is used (one after the other, each waited for a trip to memory: 8026 x
+// 5184 x 192 with an fp32 source took 157 us).  N >= 4; what lies past M or N is loaded from inside,
+// a quad that N ends in from the row's last four.
+__device__ __forceinline__ int64_t quad_inside(const BlockArgs &a, int64_t n) {
+  return n + 4 <= a.N ? n : a.N - 4;
+}
+__device__ __forceinline__ u32x4 source_at(const BlockArgs &a, int64_t m, int64_t n) {
+  const int64_t at = (m < a.M ? m : a.M - 1) * a.N + quad_inside(a, n);
+  if (a.src_bf16) {
+    const u32x2 s = *(const u32x2_any *)(a.source + at * 2);
+    return u32x4{s[0] << 16, s[0] & 0xFFFF0000u, s[1] << 16, s[1] & 0xFFFF0000u};
+  }
+  return *(const u32x4_any *)(a.source + at * 4);
+}
+// the extras of n .. n + 3, of which quad_inside() loaded x
+__device__ __forceinline__ f32x4 from_inside(const BlockArgs &a, int64_t n, u32x4 x) {
+  f32x4 v = __builtin_bit_cast(f32x4, x);
+  const int64_t by = n - quad_inside(a, n);
+  if (by == 1) v = f32x4{v[1], v[2], v[3], 0.0f};
+  if (by == 2) v = f32x4{v[2], v[3], 0.0f, 0.0f};
+  if (by == 3) v = f32x4{v[3], 0.0f, 0.0f, 0.0f};
+  return v;
+}
+__device__ __forceinline__ f32x4 bias_four(const BlockArgs &a, int64_t n) {
+  if (!a.bias) return f32x4{0, 0, 0, 0};
+  return from_inside(a, n, *(const u32x4_any *)(a.bias + quad_inside(a, n)));
+}
+__device__ __forceinline__ void put_four(const BlockArgs &a, int64_t m, int64_t n, const f32x4 &v) {
+  const int64_t at = m * a.N + n;
+  if (n + 4 <= a.N) {
+    if (a.out_bf16)
+      *(u32x2_any *)(a.C + at * 2) = u32x2{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
+    else
+      *(u32x4_any *)(a.C + at * 4) = __builtin_bit_cast(u32x4, v);
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if (n + i >= a.N) break;
+    if (a.out_bf16)
+      ((uint16_t *)a.C)[at + i] = (uint16_t)pack_bf16x2(v[i], 0.0f);
+    else
+      ((float *)a.C)[at + i] = v[i];
+  }
+}
+
 __device__ __forceinline__ void partial_four(const BlockArgs &a, int split, int64_t m, int64_t n,
                                              f32x4 v) {
   float *p = a.partials + ((int64_t)split * a.M + m) * a.N + n;

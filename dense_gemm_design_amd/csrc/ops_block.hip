@@ -223,19 +223,48 @@ __global__ void __launch_bounds__(KG *WGM *WGN * 64, 2) block_kernel(const Block
         acc[f][g] = (group ? acc[f + OWN][g] : acc[f][g]) +
                     *(f4p)(area + group * 2 * STAGE + (f * FN + g) * 1024);
   }
+  const int ml0 = wm * WM + group * OWN * 16 + r16, nl0 = wn * WN + g4 * 4;
+  if (piece >= 0 || a.N < 4) {
 #pragma unroll
-  for (int f = 0; f < OWN; ++f) {
-    const int ml = wm * WM + (group * OWN + f) * 16 + r16;
-    if (m0 + ml >= a.M) continue;
+    for (int f = 0; f < OWN; ++f) {
+      const int ml = ml0 + f * 16;
+      if (m0 + ml >= a.M) continue;
 #pragma unroll
-    for (int g = 0; g < FN; ++g) {
-      const int nl = wn * WN + g * 16 + g4 * 4;
-      if (n0 + nl >= a.N) continue;
-      if (piece >= 0)
-        *(f32x4 *)(a.partials + (int64_t)piece * (BM * BN) + ml * BN + nl) = acc[f][g];
-      else
-        store_four(a, m0 + ml, n0 + nl, acc[f][g]);
+      for (int g = 0; g < FN; ++g) {
+        const int nl = nl0 + g * 16;
+        if (n0 + nl >= a.N) continue;
+        if (piece >= 0)
+          *(f32x4 *)(a.partials + (int64_t)piece * (BM * BN) + ml * BN + nl) = acc[f][g];
+        else
+          store_four(a, m0 + ml, n0 + nl, acc[f][g]);
+      }
     }
+    return;
+  }
+  f32x4 bias[FN];
+#pragma unroll
+  for (int g = 0; g < FN; ++g) bias[g] = bias_four(a, n0 + nl0 + g * 16);
+#pragma unroll
+  for (int f0 = 0; f0 < OWN; f0 += 2) {
+    u32x4 src[2][FN];
+    if (a.source) {
+#pragma unroll
+      for (int f = 0; f < 2; ++f)
+#pragma unroll
+        for (int g = 0; g < FN; ++g)
+          src[f][g] = source_at(a, m0 + ml0 + (f0 + f) * 16, n0 + nl0 + g * 16);
+    }
+#pragma unroll
+    for (int f = 0; f < 2; ++f)
+#pragma unroll
+      for (int g = 0; g < FN; ++g) {
+        const int64_t m = m0 + ml0 + (f0 + f) * 16, n = n0 + nl0 + g * 16;
+        if (m >= a.M || n >= a.N) continue;
+        f32x4 v = acc[f0 + f][g];
+        if (a.bias) v += bias[g];
+        if (a.source) v += from_inside(a, n, src[f][g]);
+        put_four(a, m, n, v);
+      }
   }
 }
 
@@ -247,8 +276,15 @@ __global__ void __launch_bounds__(256) join_tiles_kernel(const BlockArgs a) {
   const int ml = blockIdx.x % (B / 8) * 8 + threadIdx.x / 32, nl = threadIdx.x % 32 * 4;
   int64_t m0, n0;
   tile_corner(a, a.whole + at, B, B, m0, n0);
-  if (m0 + ml >= a.M || n0 + nl >= a.N) return;
-  f32x4 v = {0, 0, 0, 0};
+  const int64_t m = m0 + ml, n = n0 + nl;
+  if (m >= a.M || n >= a.N) return;
+  const bool ahead = a.N >= 4;   // the extras are loaded before the pieces
+  u32x4 src = {0, 0, 0, 0};
+  f32x4 bias = {0, 0, 0, 0}, v = {0, 0, 0, 0};
+  if (ahead) {
+    bias = bias_four(a, n);
+    if (a.source) src = source_at(a, m, n);
+  }
   for (int s = 0; s < a.splits; s += 8) {
     f32x4 q[8];   // loads in flight together
 #pragma unroll
@@ -259,7 +295,13 @@ __global__ void __launch_bounds__(256) join_tiles_kernel(const BlockArgs a) {
 #pragma unroll
     for (int u = 0; u < 8; ++u) v += q[u];
   }
-  store_four(a, m0 + ml, n0 + nl, v);
+  if (!ahead) {
+    store_four(a, m, n, v);
+    return;
+  }
+  if (a.bias) v += bias;
+  if (a.source) v += from_inside(a, n, src);
+  put_four(a, m, n, v);
 }
 
 // Adds the splits' sums of few rows in order, then the epilogue.

@@ -461,7 +461,7 @@ BlockPlan plan_of(const gemm_block_desc &d) {
     if (splits > kb / 16) splits = kb / 16;
     return {PLAN_FEW, splits > 1 ? (int)splits : 1, 1, (int32_t)nt, 0};
   }
-  if (d.dtype_c == GEMM_BF16 && kb) {
+  if (d.dtype_c == GEMM_BF16 && kb && d.N >= 4) {   // (the wide tiles' quads want four columns)
     // Tiles of 256 x 256 (wide with powers of two, eight waves otherwise) or, for fp32 scales of 128 x
     // 128 blocks, wide ones of 192 x 256, whose round over the CUs takes 0.74 as long: 8192^3 542 us on
     // six rounds of them, 498 on four of 256; 4096 x 14336 x 4096 237 us on five, 263 on four.

@@ -251,6 +251,35 @@ def test_product_of_large_tiles(dev, M, N, K, block, pow2):
 
 @pytest.mark.parametrize("pow2", [False, True], ids=["any", "pow2"])
 @pytest.mark.parametrize("block", ["row", "tile"])
+@pytest.mark.parametrize("M,N,K", [(66000, 1, 130), (65600, 3, 200), (65700, 6, 100), (4099, 4201, 130),
+                                   (700, 903, 128), (129, 2, 4000), (256, 5, 300)])
+@pytest.mark.parametrize("source", [BF16, F32], ids=["bf16", "f32"])
+def test_product_with_extras(dev, M, N, K, block, pow2, source):
+    """Bias and source with rows that end inside four columns, and fewer columns than that."""
+    print(f"product {M}x{N}x{K} b {block} pow2={pow2}", flush=True)
+    g = gen(M + N + K)
+    a, av = operand(g, dev, M, K, "row", pow2)
+    b, bv = operand(g, dev, N, K, block, pow2)
+    av, bv = av.to(dev), bv.to(dev)
+    bias, src = randn(g, N).to(dev), randn(g, M, N).to(source).to(dev)
+    extras = [bias.double(), src.double()]
+    want = torch.mm(av, bv.t().contiguous()) + extras[0] + extras[1]
+    for dt in (BF16, F32):
+        bound = product_bound(av, bv, K, want, dt, extras)
+        whole = torch.full((M + 2, N), 7.0, dtype=dt, device=dev)
+        for into in (False, True):   # and into the source itself, where types allow
+            if into and dt is not source:
+                continue
+            if into:
+                whole[1:-1] = src
+            dg.block_gemm(a, b, bias_col=bias, source=whole[1:-1] if into else src, out=whole[1:-1])
+            bad = ~((whole[1:-1].double() - want).abs() <= bound)
+            assert not bool(bad.any()), (dt, into, int(bad.sum()), bad.nonzero()[0].tolist())
+            assert bool((whole[0] == 7).all()) and bool((whole[-1] == 7).all())
+
+
+@pytest.mark.parametrize("pow2", [False, True], ids=["any", "pow2"])
+@pytest.mark.parametrize("block", ["row", "tile"])
 @pytest.mark.parametrize("M,N,K", [(2171, 2045, 4300), (140, 139, 16000), (1300, 1300, 1100),
                                    (33, 4300, 3700)])
 def test_product_of_cut_tiles(dev, M, N, K, block, pow2):

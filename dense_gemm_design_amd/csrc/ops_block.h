@@ -66,18 +66,22 @@ __device__ __forceinline__ void store_four(const BlockArgs &a, int64_t m, int64_
 
 // The same in three steps, for kernels whose threads have many outputs: the extras are loaded for several
 // of them before the first is used (one after the other, each waited for a trip to memory: 8026 x
-// 5184 x 192 with an fp32 source took 157 us).  N >= 4; what lies past M or N is loaded from inside,
+// 5184 x 192 with an fp32 source took 157 us, 74 so).  N >= 4; what lies past M or N is loaded from inside,
 // a quad that N ends in from the row's last four.
 __device__ __forceinline__ int64_t quad_inside(const BlockArgs &a, int64_t n) {
   return n + 4 <= a.N ? n : a.N - 4;
 }
+// SRC: what the source holds, known when compiled: where two kinds of loads meet, one is waited for.
+enum { SRC_NONE, SRC_BF16, SRC_F32 };
+template <int SRC>
 __device__ __forceinline__ u32x4 source_at(const BlockArgs &a, int64_t m, int64_t n) {
   const int64_t at = (m < a.M ? m : a.M - 1) * a.N + quad_inside(a, n);
-  if (a.src_bf16) {
+  if constexpr (SRC == SRC_BF16) {
     const u32x2 s = *(const u32x2_any *)(a.source + at * 2);
-    return u32x4{s[0] << 16, s[0] & 0xFFFF0000u, s[1] << 16, s[1] & 0xFFFF0000u};
+    return u32x4{s[0], s[1], 0, 0};
+  } else {
+    return *(const u32x4_any *)(a.source + at * 4);
   }
-  return *(const u32x4_any *)(a.source + at * 4);
 }
 // the extras of n .. n + 3, of which quad_inside() loaded x
 __device__ __forceinline__ f32x4 from_inside(const BlockArgs &a, int64_t n, u32x4 x) {
@@ -87,6 +91,21 @@ __device__ __forceinline__ f32x4 from_inside(const BlockArgs &a, int64_t n, u32x
   if (by == 2) v = f32x4{v[2], v[3], 0.0f, 0.0f};
   if (by == 3) v = f32x4{v[3], 0.0f, 0.0f, 0.0f};
   return v;
+}
+template <int SRC>
+__device__ __forceinline__ f32x4 source_four(const BlockArgs &a, int64_t n, u32x4 s) {
+  if constexpr (SRC == SRC_BF16)
+    s = u32x4{s[0] << 16, s[0] & 0xFFFF0000u, s[1] << 16, s[1] & 0xFFFF0000u};
+  return from_inside(a, n, s);
+}
+template <class F>
+__device__ __forceinline__ void with_source(const BlockArgs &a, F f) {
+  if (!a.source)
+    f(std::integral_constant<int, SRC_NONE>());
+  else if (a.src_bf16)
+    f(std::integral_constant<int, SRC_BF16>());
+  else
+    f(std::integral_constant<int, SRC_F32>());
 }
 __device__ __forceinline__ f32x4 bias_four(const BlockArgs &a, int64_t n) {
   if (!a.bias) return f32x4{0, 0, 0, 0};

@@ -244,28 +244,31 @@ __global__ void __launch_bounds__(KG *WGM *WGN * 64, 2) block_kernel(const Block
   f32x4 bias[FN];
 #pragma unroll
   for (int g = 0; g < FN; ++g) bias[g] = bias_four(a, n0 + nl0 + g * 16);
+  with_source(a, [&](auto src_c) {
+    constexpr int SRC = decltype(src_c)::value;
 #pragma unroll
-  for (int f0 = 0; f0 < OWN; f0 += 2) {
-    u32x4 src[2][FN];
-    if (a.source) {
+    for (int f0 = 0; f0 < OWN; f0 += 2) {
+      u32x4 src[2][FN];
+      if constexpr (SRC != SRC_NONE) {
+#pragma unroll
+        for (int f = 0; f < 2; ++f)
+#pragma unroll
+          for (int g = 0; g < FN; ++g)
+            src[f][g] = source_at<SRC>(a, m0 + ml0 + (f0 + f) * 16, n0 + nl0 + g * 16);
+      }
 #pragma unroll
       for (int f = 0; f < 2; ++f)
 #pragma unroll
-        for (int g = 0; g < FN; ++g)
-          src[f][g] = source_at(a, m0 + ml0 + (f0 + f) * 16, n0 + nl0 + g * 16);
+        for (int g = 0; g < FN; ++g) {
+          const int64_t m = m0 + ml0 + (f0 + f) * 16, n = n0 + nl0 + g * 16;
+          if (m >= a.M || n >= a.N) continue;
+          f32x4 v = acc[f0 + f][g];
+          if (a.bias) v += bias[g];
+          if constexpr (SRC != SRC_NONE) v += source_four<SRC>(a, n, src[f][g]);
+          put_four(a, m, n, v);
+        }
     }
-#pragma unroll
-    for (int f = 0; f < 2; ++f)
-#pragma unroll
-      for (int g = 0; g < FN; ++g) {
-        const int64_t m = m0 + ml0 + (f0 + f) * 16, n = n0 + nl0 + g * 16;
-        if (m >= a.M || n >= a.N) continue;
-        f32x4 v = acc[f0 + f][g];
-        if (a.bias) v += bias[g];
-        if (a.source) v += from_inside(a, n, src[f][g]);
-        put_four(a, m, n, v);
-      }
-  }
+  });
 }
 
 // Adds the pieces of the tiles whose K is cut, in order, then the epilogue.  Eight rows of a tile a
@@ -279,29 +282,32 @@ __global__ void __launch_bounds__(256) join_tiles_kernel(const BlockArgs a) {
   const int64_t m = m0 + ml, n = n0 + nl;
   if (m >= a.M || n >= a.N) return;
   const bool ahead = a.N >= 4;   // the extras are loaded before the pieces
-  u32x4 src = {0, 0, 0, 0};
-  f32x4 bias = {0, 0, 0, 0}, v = {0, 0, 0, 0};
-  if (ahead) {
-    bias = bias_four(a, n);
-    if (a.source) src = source_at(a, m, n);
-  }
-  for (int s = 0; s < a.splits; s += 8) {
-    f32x4 q[8];   // loads in flight together
+  with_source(a, [&](auto src_c) {
+    constexpr int SRC = decltype(src_c)::value;
+    u32x4 src;
+    f32x4 bias = {0, 0, 0, 0}, v = {0, 0, 0, 0};
+    if (ahead) {
+      bias = bias_four(a, n);
+      if constexpr (SRC != SRC_NONE) src = source_at<SRC>(a, m, n);
+    }
+    for (int s = 0; s < a.splits; s += 8) {
+      f32x4 q[8];   // loads in flight together
 #pragma unroll
-    for (int u = 0; u < 8; ++u)
-      q[u] = s + u < a.splits ? *(const f32x4 *)(a.partials + (int64_t)((s + u) * cut + at) * (B * B) +
-                                                 ml * B + nl)
-                              : f32x4{0, 0, 0, 0};
+      for (int u = 0; u < 8; ++u)
+        q[u] = s + u < a.splits
+                   ? *(const f32x4 *)(a.partials + (int64_t)((s + u) * cut + at) * (B * B) + ml * B + nl)
+                   : f32x4{0, 0, 0, 0};
 #pragma unroll
-    for (int u = 0; u < 8; ++u) v += q[u];
-  }
-  if (!ahead) {
-    store_four(a, m, n, v);
-    return;
-  }
-  if (a.bias) v += bias;
-  if (a.source) v += from_inside(a, n, src);
-  put_four(a, m, n, v);
+      for (int u = 0; u < 8; ++u) v += q[u];
+    }
+    if (!ahead) {
+      store_four(a, m, n, v);
+      return;
+    }
+    if (a.bias) v += bias;
+    if constexpr (SRC != SRC_NONE) v += source_four<SRC>(a, n, src);
+    put_four(a, m, n, v);
+  });
 }
 
 // Adds the splits' sums of few rows in order, then the epilogue.

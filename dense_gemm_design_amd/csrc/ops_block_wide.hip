@@ -462,42 +462,45 @@ wide_block_kernel(const BlockArgs a) {
     // With a source, or rows that are not 16-byte aligned: through the wave's LDS as fp32,
     // half a row of blocks at a time, the source's next half on its way.
     out.clear(a);
-    constexpr int QUADS = WN / 8, U = 16 * QUADS / 64;   // of half a row: a row's, and a lane's
-    f32x4 bias[2];
-    u32x4 src[2][U];
-    const int64_t lm = tm + lane / QUADS, ln = tn + lane % QUADS * 4;
-    auto fetch = [&](auto i_c) {
-      constexpr int f = decltype(i_c)::value / 2, h = decltype(i_c)::value % 2;
+    with_source(a, [&](auto src_c) {
+      constexpr int SRC = decltype(src_c)::value;
+      constexpr int QUADS = WN / 8, U = 16 * QUADS / 64;   // of half a row: a row's, and a lane's
+      f32x4 bias[2];
+      u32x4 src[2][U];
+      const int64_t lm = tm + lane / QUADS, ln = tn + lane % QUADS * 4;
+      auto fetch = [&](auto i_c) {
+        constexpr int f = decltype(i_c)::value / 2, h = decltype(i_c)::value % 2;
 #pragma unroll
-      for (int u = 0; u < U; ++u)
-        src[h][u] = source_at(a, lm + f * 16 + u * (16 / U), ln + h * (WN / 2));
-    };
+        for (int u = 0; u < U; ++u)
+          src[h][u] = source_at<SRC>(a, lm + f * 16 + u * (16 / U), ln + h * (WN / 2));
+      };
 #pragma unroll
-    for (int h = 0; h < 2; ++h) bias[h] = bias_four(a, ln + h * (WN / 2));
-    if (a.source) fetch(std::integral_constant<int, 0>());
-    [&]<int... I>(std::integer_sequence<int, I...>) {
-      (
-          [&] {
-            constexpr int f = I / 2, h = I % 2, PITCH = (WN / 2 + 4) * 4;
-            [&]<int... E>(std::integer_sequence<int, E...>) {
-              ((*(f4p)(slice + r16 * PITCH + E * 64 + g4 * 16) =
-                    quad_of<POW2>(acc[f][h * (FN / 2) + E], 0)),
-               ...);
-            }(std::make_integer_sequence<int, FN / 2>());
-            if (I + 1 < 2 * FM && a.source)
-              fetch(std::integral_constant<int, I + 1 < 2 * FM ? I + 1 : I>());
+      for (int h = 0; h < 2; ++h) bias[h] = bias_four(a, ln + h * (WN / 2));
+      if constexpr (SRC != SRC_NONE) fetch(std::integral_constant<int, 0>());
+      [&]<int... I>(std::integer_sequence<int, I...>) {
+        (
+            [&] {
+              constexpr int f = I / 2, h = I % 2, PITCH = (WN / 2 + 4) * 4;
+              [&]<int... E>(std::integer_sequence<int, E...>) {
+                ((*(f4p)(slice + r16 * PITCH + E * 64 + g4 * 16) =
+                      quad_of<POW2>(acc[f][h * (FN / 2) + E], 0)),
+                 ...);
+              }(std::make_integer_sequence<int, FN / 2>());
+              if constexpr (I + 1 < 2 * FM && SRC != SRC_NONE)
+                fetch(std::integral_constant<int, I + 1 < 2 * FM ? I + 1 : I>());
 #pragma unroll
-            for (int u = 0; u < U; ++u) {
-              const int64_t m = lm + f * 16 + u * (16 / U), n = ln + h * (WN / 2);
-              f32x4 v = *(f4p)(slice + (lane / QUADS + u * (16 / U)) * PITCH + lane % QUADS * 16);
-              if (a.bias) v += bias[h];
-              if (a.source) v += from_inside(a, n, src[h][u]);
-              if (m < a.M && n < a.N) put_four(a, m, n, v);
-            }
-            __builtin_amdgcn_sched_barrier(0);
-          }(),
-          ...);
-    }(std::make_integer_sequence<int, 2 * FM>());
+              for (int u = 0; u < U; ++u) {
+                const int64_t m = lm + f * 16 + u * (16 / U), n = ln + h * (WN / 2);
+                f32x4 v = *(f4p)(slice + (lane / QUADS + u * (16 / U)) * PITCH + lane % QUADS * 16);
+                if (a.bias) v += bias[h];
+                if constexpr (SRC != SRC_NONE) v += source_four<SRC>(a, n, src[h][u]);
+                if (m < a.M && n < a.N) put_four(a, m, n, v);
+              }
+              __builtin_amdgcn_sched_barrier(0);
+            }(),
+            ...);
+      }(std::make_integer_sequence<int, 2 * FM>());
+    });
   }
   wait_vmcnt<0>();   // no load is on its way into LDS that the workgroup no longer has
 }

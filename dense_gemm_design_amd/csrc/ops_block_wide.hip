@@ -6,8 +6,9 @@
 // two rows of blocks are taken column by column, so that the reads of B's fragments have 16 slots,
 // about what LDS takes for them, and 14 more before their next MFMA.
 //  * Powers of two, 256 x 256: the 256 accumulators of a lane stay in accumulation registers, and
-//    the MFMA adds to them.  8192^3 in 380 us, 2.9 PFLOP/s; the matrix units are busy 0.66 of the time
-//    at the 2.05 GHz that the card then holds.
+//    the MFMA adds to them.  8192^3 in 401 us on inputs that change from call to call, 2.74 PFLOP/s (the
+//    product with one scale a tensor takes as long); the matrix units are busy 0.70 of the time, at the
+//    2.01 GHz that the card then holds.
 //  * fp32 scales of 128 x 128 blocks of B, 192 x 256: vector instructions reach only the other 256
 //    registers, so there the 192 accumulators have to be, and the fragments go to the accumulation
 //    registers.  A wave's columns are one block of B, so its scales are one a row.  An MFMA's four

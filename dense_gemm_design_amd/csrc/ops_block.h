@@ -145,28 +145,72 @@ __device__ __forceinline__ void partial_four(const BlockArgs &a, int split, int6
 // The exponent byte of a power of two, in every byte-position the MFMA may be told to read: byte 0.
 __device__ __forceinline__ int exponent_of(float s) { return (int)(__float_as_uint(s) >> 23); }
 
-__device__ __forceinline__ f32x4 mfma_block(const i32x8 &b, const i32x8 &a) {
-  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(b, a, f32x4{0, 0, 0, 0}, 0, 0, 0, 0, 0,
-                                                          0);
-}
 __device__ __forceinline__ f32x4 mfma_block_scaled(const i32x8 &b, const i32x8 &a, const f32x4 &c,
                                                    int eb, int ea) {
   return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(b, a, c, 0, 0, 0, eb, 0, ea);
 }
 
-// The codes of a fragment as bf16, eight a vector.
+// ---- fp32 scales of any size ------------------------------------------------------------------
+//
+// A term is P sa sb, where P, a block's sum, is zero or between 2^-18 and 2^25.  sa sb alone may pass
+// the largest number (and 0 inf is NaN) or fall under the smallest normal one, and so may P times
+// either scale, where the term itself does neither.  So one scale gives a power of two to the matrix
+// unit, which applies it to P without rounding, s = 2^h m with h between -100 and 100, and what is left
+// stays in range:
+//  * B scaled by tiles: sb = 2^h m, m from 1/2 to 1, and the term is (2^h P) (sa m);
+//  * B scaled by rows: sa = 2^h m, m from 1 to 2, and the term is ((2^h P) sb) m.
+// Where h is at its bound, m is outside these.  Then sa m may still pass the largest number, and is cut
+// to it: 2^h is 2^100, and the term zero if P is, and itself past the largest number if not.  (Whatever
+// else leaves the range then does so in terms that leave it.)
+__device__ __forceinline__ int scale_byte(float s, int more) {   // h + 127, the MFMA's e8m0
+  const int e = (int)(__float_as_uint(s) >> 23 & 255) + more;
+  return e < 27 ? 27 : e > 227 ? 227 : e;
+}
+__device__ __forceinline__ float scale_rest(float s, int byte) {   // m, exact
+  return s * __uint_as_float((uint32_t)(254 - byte) << 23);
+}
+__device__ __forceinline__ float power_of(int byte) { return __uint_as_float((uint32_t)byte << 23); }
+
+struct TileScale {   // of B, the same in all lanes: the work on it is the scalar unit's
+  uint32_t bytes;    // of B's power, and 1, for the MFMA to pick from
+  float rest, most;
+  __device__ __forceinline__ explicit TileScale(int bits) {
+    const float s = __int_as_float(__builtin_amdgcn_readfirstlane(bits));
+    const int byte = scale_byte(s, 1);
+    bytes = (uint32_t)byte | 127u << 8;
+    rest = scale_rest(s, byte);
+    const bool large = byte == 227 && fabsf(s) < __builtin_inff();
+    most = large ? 0x1.fffffep127f : __builtin_inff();
+  }
+  __device__ __forceinline__ float power() const { return power_of(bytes & 255); }
+  __device__ __forceinline__ float times(float sa) const {   // a NaN stays
+    return __builtin_elementwise_maximum(__builtin_elementwise_minimum(sa * rest, most), -most);
+  }
+};
+
+// 2^(byte - 127) P, the byte that of a's scale, or TileScale's of b's
+__device__ __forceinline__ f32x4 mfma_block_a(const i32x8 &b, const i32x8 &a, int byte) {
+  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(b, a, f32x4{0, 0, 0, 0}, 0, 0, 0, 127, 0,
+                                                          byte);
+}
+__device__ __forceinline__ f32x4 mfma_block_b(const i32x8 &b, const i32x8 &a, uint32_t bytes) {
+  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(b, a, f32x4{0, 0, 0, 0}, 0, 0, 0,
+                                                          (int)bytes, 1, (int)bytes);
+}
+
+// The codes of a fragment, times a power of two, as bf16, eight a vector.
 struct BlockBf16 {
   bf16x8 v[4];
 };
-__device__ __forceinline__ BlockBf16 widen(const i32x8 &q) {
+__device__ __forceinline__ BlockBf16 widen(const i32x8 &q, float power) {
   typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
   BlockBf16 r;
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
-    const bf16x2 a = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(q[2 * j], 1.0f, false);
-    const bf16x2 b = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(q[2 * j], 1.0f, true);
-    const bf16x2 c = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(q[2 * j + 1], 1.0f, false);
-    const bf16x2 d = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(q[2 * j + 1], 1.0f, true);
+    const bf16x2 a = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(q[2 * j], power, false);
+    const bf16x2 b = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(q[2 * j], power, true);
+    const bf16x2 c = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(q[2 * j + 1], power, false);
+    const bf16x2 d = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(q[2 * j + 1], power, true);
     r.v[j] = bf16x8{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
   }
   return r;

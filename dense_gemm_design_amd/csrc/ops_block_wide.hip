@@ -11,10 +11,10 @@
 //    2.01 GHz that the card then holds.
 //  * fp32 scales of 128 x 128 blocks of B, 192 x 256: vector instructions reach only the other 256
 //    registers, so there the 192 accumulators have to be, and the fragments go to the accumulation
-//    registers.  A wave's columns are one block of B, so its scales are one a row.  An MFMA's four
-//    results are added two slots later, when they have left the matrix unit.  4096 x 14336 x 4096 in
-//    228 us, 2.1 PFLOP/s: with one wave a SIMD an instruction takes four cycles to issue, and the 430
-//    of a step, 192 of them these additions, take longer than its 48 MFMAs.
+//    registers.  A wave's columns are one block of B, whose power of two the MFMA applies; what is left of
+//    that scale, times A's, is one a row.  An MFMA's four results are added two slots later, when they
+//    have left the matrix unit.  4096 x 14336 x 4096 in 250 to 270 us by the card, 1.8 to 1.9 PFLOP/s
+//    (4 % less time with the scales' product formed first, which left the range of fp32 where C does not).
 // Workgroups stay for tile after tile: the loads of the next one are under way when a tile ends, and
 // what a tile leaves in the registers is written out beside the next one's first step (written at
 // once by all CUs, the 33 MB of a round took 8 us in which nothing was multiplied).
@@ -275,9 +275,11 @@ wide_block_kernel(const BlockArgs a) {
   i32x8 fa[FM], fb[FN];
   f32x4 acc[FM][FN], p[4];
   // The next step's scales as they are in memory, one of 64 rows (columns) a lane, and this step's in
-  // use: exponents (POW2), or A's times B's, spread to the lanes of each block's rows.
+  // use: exponents (POW2), or A's times what is left of B's, spread to the lanes of each block's rows,
+  // and the power of two of B's.
   constexpr int XB = ROWB ? 2 : 1;
   int raw_a[2], raw_b[XB], sa[8], sb[ROWB ? 8 : 1];
+  TileScale tile(0);
   auto read_a = [&](const lds_t *st, int f) {
     fa[f] = lds_frag<DT_FP8>(st + arow + c0 + f * 2048, st + arow + c1 + f * 2048);
   };
@@ -309,13 +311,15 @@ wide_block_kernel(const BlockArgs a) {
     if constexpr (POW2)
       spread((int)((uint32_t)raw_a[x] >> 23), sa + 4 * x);
     else
-      spread(__float_as_int(__int_as_float(raw_a[x]) * __int_as_float(raw_b[0])), sa + 4 * x);
+      spread(__float_as_int(tile.times(__int_as_float(raw_a[x]))), sa + 4 * x);
   };
   auto use_b = [&](int x) {
     if constexpr (ROWB)
       spread((int)((uint32_t)raw_b[x] >> 23), sb + 4 * x);
     else if constexpr (POW2)
       sb[0] = (int)((uint32_t)raw_b[0] >> 23);
+    else
+      sb[0] = (int)tile.bytes;
   };
 
   int c = 0;
@@ -341,6 +345,7 @@ wide_block_kernel(const BlockArgs a) {
   for (int f = 0; f < FM; ++f) read_a(smem, f);
   cs = ps;
   end();
+  if constexpr (!POW2) tile = TileScale(raw_b[0]);
   use_a(0);
   use_b(0);
 
@@ -384,7 +389,9 @@ wide_block_kernel(const BlockArgs a) {
           [&] {
             constexpr int i = I, f = O::row(i), g = O::col(i);
             if constexpr (!POW2) {
-              p[i % 4] = mfma_block(fb[g], fa[f]);
+              p[i % 4] = mfma_block_b(fb[g], fa[f], sb[0]);
+              // results that are added in the next step: their MFMAs must not be moved there
+              if constexpr (i >= NM - 2) asm volatile("" : "+v"(p[i % 4]));
               __builtin_amdgcn_sched_barrier(0);   // before what follows, which counts on it
               if constexpr (i >= 2)
                 add(O(), std::integral_constant<int, i - 2>(), first_c);
@@ -402,6 +409,7 @@ wide_block_kernel(const BlockArgs a) {
               scales_at(cs);
             }
             if constexpr (i >= 4 && i - 4 < XB + 2) read_scale(i - 4);
+            if constexpr (!POW2 && i == NM - 4) tile = TileScale(raw_b[0]);
             if constexpr (i == NM - 4) use_a(0);
             if constexpr (ROWB && i == NM - 3) use_b(0);
             if constexpr (i == HS) handshake(c + 1, std::integral_constant<int, XB + 2>());

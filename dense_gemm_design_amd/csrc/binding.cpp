@@ -439,13 +439,16 @@ PyObject *norm(PyObject *, PyObject *const *arg, Py_ssize_t) {
     const Stream s(device);
     at::Tensor out = make(first, {}, at::kFloat);
     const Workspace w(first, need);
-    if (clip)
-      ok(gemm_clip_grad_norm(list.data(), count, (float)max_norm, (float *)out.data_ptr(), w.ptr,
-                             w.bytes, s.ptr),
-         "gemm_clip_grad_norm");
-    else
+    if (clip) {
+      const int st = gemm_clip_grad_norm(list.data(), count, (float)max_norm,
+                                         (float *)out.data_ptr(), w.ptr, w.bytes, s.ptr);
+      if (st == GEMM_ERR_INVALID_ARG)   // what else is invalid has been refused above
+        throw Refused("what is written for one gradient overlaps another one, or its output");
+      ok(st, "gemm_clip_grad_norm");
+    } else {
       ok(gemm_grad_norm(list.data(), count, (float *)out.data_ptr(), w.ptr, w.bytes, s.ptr),
          "gemm_grad_norm");
+    }
     PyObject *r = THPVariable_Wrap(out);
     if (!r) throw PythonError{};
     return r;

@@ -161,5 +161,6 @@ def grad_norm(grads):
 
 def clip_grad_norm(grads, max_norm, out=None):
     """Scales a list of gradients by min(1, max_norm / (norm + 1e-6)), in place or into the tensors
-    `out` (one of each gradient's type and size), and returns the norm before that, as grad_norm."""
+    `out` (one of each gradient's type and size), and returns the norm before that, as grad_norm.  What
+    is written for one gradient must not overlap another one (a gradient that is in the list twice)."""
     return _binding().norm(grads, out, max_norm)

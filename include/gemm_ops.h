@@ -101,7 +101,9 @@ int gemm_grad_norm_workspace(const gemm_tensor *list, int64_t count, size_t *byt
 int gemm_grad_norm(const gemm_tensor *list, int64_t count, float *norm, void *workspace,
                    size_t workspace_bytes, void *stream);
 
-/* The same, and out = data * min(1, max_norm / (norm + 1e-6)) for every tensor. */
+/* The same, and out = data * min(1, max_norm / (norm + 1e-6)) for every tensor.  An output may be its own
+ * data; one that overlaps anything else of the list (a tensor that is in it twice, in place) is
+ * GEMM_ERR_INVALID_ARG. */
 int gemm_clip_grad_norm(const gemm_tensor *list, int64_t count, float max_norm, float *norm,
                         void *workspace, size_t workspace_bytes, void *stream);
 

@@ -1,0 +1,72 @@
+"""Outputs that overlap what other workgroups still read or write are refused (C ABI, on the CPU: every call
+here returns before anything is enqueued)."""
+import ctypes
+import random
+
+import pytest
+
+torch = pytest.importorskip("torch")
+
+from dense_gemm_design_amd import _lib as L  # noqa: E402
+from dense_gemm_design_amd import ops as O  # noqa: E402
+
+P = 1 << 20
+
+
+def clip(entries):
+    """Status of a clipping call without a workspace, so that a list that is in order gets no further."""
+    arr = (O.GemmTensor * len(entries))(*[O.GemmTensor(*e) for e in entries])
+    return O.load().gemm_clip_grad_norm(arr, len(entries), 1.0, P, None, 0, None)
+
+
+def test_clip_refuses_what_overlaps():
+    inv, ok = L.GEMM_ERR_INVALID_ARG, L.GEMM_ERR_WORKSPACE
+    f32, bf16 = L.GEMM_F32, L.GEMM_BF16
+    g, h, o, q = P, P + (1 << 16), P + (2 << 16), P + (3 << 16)
+    n = 100
+    for entries, want in (
+            ([(g, g, n, f32), (h, h, n, f32)], ok),
+            ([(h, h, n, f32), (g, g, n, f32)], ok),
+            ([(g, g, n, f32), (g, g, n, f32)], inv),                  # twice, in place
+            ([(g, o, n, f32), (g, q, n, f32)], ok),                   # twice, out of place
+            ([(g, o, n, f32), (h, o, n, f32)], inv),                  # one output for two
+            ([(g, h, n, f32), (h, g, n, f32)], inv),                  # outputs exchanged
+            ([(g, g + 16, n, f32)], inv),                             # shifted over its own data
+            ([(g, g - 16, n, f32)], inv),
+            ([(g, g, n, f32), (g + 4 * n, g + 4 * n, n, f32)], ok),   # neighbours
+            ([(g, g, n, f32), (g + 4 * n - 2, g + 4 * n - 2, n, bf16)], inv),
+            ([(g, g, n, bf16), (g + 2 * n, g + 2 * n, n, bf16)], ok),
+            ([(g, g, n, f32), (g + 40, o, 3, f32)], inv),             # inside what is scaled in place
+            ([(g, g, n, f32), (g + 40, g + 40, 0, f32)], ok),         # of nothing
+            ([(g, o, n, f32), (g + 40, q, 3, f32)], ok)):             # inside what is only read
+        assert clip(entries) == want, entries
+
+
+@pytest.mark.parametrize("into", [False, True], ids=["in_place", "into"])
+@pytest.mark.parametrize("order", ["rising", "falling", "mixed", "two buffers"])
+def test_clip_finds_an_overlap_in_long_lists(order, into):
+    rng = random.Random(len(order))
+    sizes = [rng.randint(1, 3000) for _ in range(300)]
+    at, entries, far = P, [], 1 << 36
+    for k, n in enumerate(sizes):
+        t = L.GEMM_F32 if k % 3 else L.GEMM_BF16
+        base = at if order != "two buffers" or t == L.GEMM_F32 else at + (1 << 34)
+        entries.append((base, base + far if into else base, n, t))
+        at = (at + n * (4 if t == L.GEMM_F32 else 2) + 3) // 4 * 4 + rng.choice([0, 256])
+    if order == "falling":
+        entries.reverse()
+    if order == "mixed":
+        rng.shuffle(entries)
+    assert clip(entries) == L.GEMM_ERR_WORKSPACE
+    for _ in range(20):
+        i, j = rng.sample(range(300), 2)
+        bad = list(entries)
+        d, o, n, t = bad[i]
+        es = 4 if t == L.GEMM_F32 else 2
+        other = bad[j]
+        width = other[2] * (4 if other[3] == L.GEMM_F32 else 2)
+        # i's output begins within, or ends within, what is written for j
+        begin = other[1] + (rng.randrange(0, width, 4) if rng.random() < 0.5 else -rng.randrange(0, n * es, 4))
+        bad[i] = (d if into else begin, begin, n, t)
+        if begin + n * es > other[1]:
+            assert clip(bad) == L.GEMM_ERR_INVALID_ARG, (i, j)

@@ -544,6 +544,18 @@ bool types_ok(int dtype, int wtype) {
 bool stride_ok(int64_t rows, int64_t cols, int64_t stride) {
   return stride >= 0 && (rows <= 1 || stride == 0 || stride >= cols);
 }
+// Whether packed rows may be written to `to` while rows of `from` are read: apart from each of them, or each
+// over its own.  (Over rows with another stride, a workgroup's row would fall on one that another workgroup
+// has yet to read.)
+bool apart_or_same(const void *to, const void *from, int64_t rows, int64_t cols, int64_t stride,
+                   size_t es) {
+  if (to == from && (rows <= 1 || stride == cols)) return true;
+  const uintptr_t t0 = (uintptr_t)to, t1 = t0 + (uintptr_t)(rows * cols) * es, f0 = (uintptr_t)from;
+  const uintptr_t row = (uintptr_t)cols * es, step = (uintptr_t)stride * es;
+  if (rows <= 1 || stride == 0) return t1 <= f0 || f0 + row <= t0;
+  const uintptr_t r = t0 < f0 + row ? 0 : (t0 - f0 - row) / step + 1;   // the first row that ends behind t0
+  return r >= (uintptr_t)rows || f0 + r * step >= t1;
+}
 
 }  // namespace
 }  // namespace dg
@@ -603,6 +615,9 @@ extern "C" int gemm_layer_norm_backward(const void *dy, int64_t dstride, const v
       !aligned(w, elem(wtype)) || !aligned(dw, elem(wtype)) || !aligned(db, elem(wtype)) ||
       !aligned(mean, 4) || !aligned(rstd, 4) || !aligned(workspace, 16))
     return GEMM_ERR_ALIGNMENT;
+  if (rows > 0 && (!apart_or_same(dx, x, rows, cols, stride, elem(dtype)) ||
+                   !apart_or_same(dx, dy, rows, cols, dstride, elem(dtype))))
+    return GEMM_ERR_INVALID_ARG;
   size_t need = 0;
   gemm_layer_norm_backward_workspace(rows, cols, &need);
   if (need && (!workspace || workspace_bytes < need)) return GEMM_ERR_WORKSPACE;

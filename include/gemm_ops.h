@@ -80,7 +80,8 @@ int gemm_layer_norm(const void *x, int dtype, int64_t rows, int64_t cols, int64_
 int gemm_layer_norm_backward_workspace(int64_t rows, int64_t cols, size_t *bytes);
 
 /* Gradients of gemm_layer_norm for the gradient dy of y: dx (dtype, packed rows), dw and db
- * (wtype, cols elements; summed over the rows in fp32).  dx may be dy or x itself. */
+ * (wtype, cols elements; summed over the rows in fp32).  dx may be dy or x itself if that has packed rows;
+ * where it overlaps rows of theirs otherwise, GEMM_ERR_INVALID_ARG. */
 int gemm_layer_norm_backward(const void *dy, int64_t dy_stride, const void *x, int64_t x_stride,
                              int dtype, int64_t rows, int64_t cols, const void *w, int wtype,
                              const float *mean, const float *rstd, void *dx, void *dw, void *db,

@@ -70,3 +70,48 @@ def test_clip_finds_an_overlap_in_long_lists(order, into):
         bad[i] = (d if into else begin, begin, n, t)
         if begin + n * es > other[1]:
             assert clip(bad) == L.GEMM_ERR_INVALID_ARG, (i, j)
+
+
+def back(dx, dy, dstride, x, stride, rows=5, cols=64, dtype=L.GEMM_F32):
+    """Status of a norm's backward pass without a workspace."""
+    w = P << 8
+    return O.load().gemm_layer_norm_backward(dy, dstride, x, stride, dtype, rows, cols, w, L.GEMM_F32, w, w,
+                                             dx, w, w, None, 0, None)
+
+
+def test_norm_backward_refuses_a_dx_over_rows_of_another_stride():
+    inv, ok = L.GEMM_ERR_INVALID_ARG, L.GEMM_ERR_WORKSPACE
+    x, dy = P, P + (1 << 20)
+    row = 64 * 4
+    for args, want in (((dy + (1 << 20), dy, 64, x, 64), ok),
+                       ((x, dy, 64, x, 64), ok), ((dy, dy, 64, x, 64), ok),      # each row over its own
+                       ((x, dy, 64, x, 65), inv), ((x, dy, 64, x, 128), inv),
+                       ((dy, dy, 65, x, 64), inv), ((dy, dy, 0, x, 64), inv),    # one row for all
+                       ((x, dy, 64, x, 0), inv),
+                       ((x + row, dy, 64, x, 64), inv), ((x - row, dy, 64, x, 64), inv),
+                       ((x + 5 * row, dy, 64, x, 64), ok), ((x - 5 * row, dy, 64, x, 64), ok),
+                       ((x + 5 * row - 4, dy, 64, x, 64), inv), ((x - 5 * row + 4, dy, 64, x, 64), inv),
+                       ((x + row, dy, 64, x, 64 * 6), ok),                        # between two rows
+                       ((x + row, dy, 64, x, 64 * 6 - 1), inv),
+                       ((x + 2 * 6 * row + row, dy, 64, x, 64 * 6), ok),
+                       ((x + 2 * 6 * row + row - 4, dy, 64, x, 64 * 6), inv),
+                       ((x + 4 * 6 * row + row, dy, 64, x, 64 * 6), ok),          # behind the last
+                       ((dy, dy, 0, x, 64, 1), ok), ((x, dy, 64, x, 99, 1), ok)):  # one row: no stride
+        assert back(*args) == want, args
+
+
+def test_norm_backward_overlaps_against_plain_sets():
+    rng = random.Random(3)
+    far = P << 4
+    for _ in range(3000):
+        rows, cols = rng.randint(1, 5), rng.randint(1, 6)
+        stride = rng.choice([0, cols, cols + rng.randint(1, 40)])
+        at = rng.randint(-60, 200)
+        own = {e for r in range(rows) for e in range(r * stride, r * stride + cols)}
+        out = set(range(at, at + rows * cols))
+        want = not (own & out) or (at == 0 and (rows == 1 or stride == cols))
+        for dtype, es in ((L.GEMM_F32, 4), (L.GEMM_BF16, 2)):
+            got = back(P + at * es, far, cols, P, stride, rows, cols, dtype)
+            assert got == (L.GEMM_ERR_WORKSPACE if want else L.GEMM_ERR_INVALID_ARG), (rows, cols, stride, at)
+            got = back(P + at * es, P, stride, far, cols, rows, cols, dtype)
+            assert got == (L.GEMM_ERR_WORKSPACE if want else L.GEMM_ERR_INVALID_ARG), (rows, cols, stride, at)

@@ -296,10 +296,13 @@ PyObject *block_gemm(PyObject *, PyObject *const *arg, Py_ssize_t) {
       ok(gemm_block_workspace(&d, &need), "gemm_block_workspace");
       const Stream s(on.device);
       const Workspace w(a.data, need);
-      ok(gemm_block_run(&d, a.data.data_ptr(), (const float *)a.scales.data_ptr(),
-                        b.data.data_ptr(), (const float *)b.scales.data_ptr(), out.data_ptr(),
-                        (const float *)data(bias), data(source), w.ptr, w.bytes, s.ptr),
-         "gemm_block_run");
+      const int st = gemm_block_run(&d, a.data.data_ptr(), (const float *)a.scales.data_ptr(),
+                                    b.data.data_ptr(), (const float *)b.scales.data_ptr(),
+                                    out.data_ptr(), (const float *)data(bias), data(source), w.ptr,
+                                    w.bytes, s.ptr);
+      if (st == GEMM_ERR_INVALID_ARG)   // what else is invalid has been refused above
+        throw Refused("out overlaps source, or bias_col, and is not the source itself");
+      ok(st, "gemm_block_run");
     }
     PyObject *r = THPVariable_Wrap(out);
     if (!r) throw PythonError{};

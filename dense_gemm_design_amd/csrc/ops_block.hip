@@ -607,6 +607,17 @@ extern "C" int gemm_block_run(const gemm_block_desc *d, const void *A, const flo
       ((uintptr_t)scale_b & 3) || ((uintptr_t)bias & 3) || ((uintptr_t)C & out) ||
       ((uintptr_t)source & in) || ((uintptr_t)workspace & 15))
     return GEMM_ERR_ALIGNMENT;
+  // an element of the source is read before that of C is written, by the same lane; any other overlap would
+  // be read by one workgroup and written by another
+  const uintptr_t c0 = (uintptr_t)C, c1 = c0 + (uintptr_t)(d->M * d->N) * (out + 1);
+  const auto apart = [&](const void *p, int64_t n, uintptr_t es) {
+    const uintptr_t p0 = (uintptr_t)p;
+    return !p || p0 >= c1 || p0 + (uintptr_t)n * es <= c0;
+  };
+  if (!(source == C && d->dtype_source == d->dtype_c) && !apart(source, d->M * d->N, in + 1))
+    return GEMM_ERR_INVALID_ARG;
+  if (!(bias == C && d->M == 1 && d->dtype_c == GEMM_F32) && !apart(bias, d->N, 4))
+    return GEMM_ERR_INVALID_ARG;
   const BlockPlan p = plan_of(*d);
   size_t need = 0;
   gemm_block_workspace(d, &need);

@@ -121,7 +121,7 @@ def block_quantize(x, block="row", transposed=False, pow2=False):
 def block_gemm(a, b, out_dtype="bf16", bias_col=None, source=None, out=None):
     """C (M, N) = A B^T + bias_col + source of BlockScaled operands a (M, K), scaled per row and
     block of 128, and b (N, K), scaled per row or per tile.  bias_col: N float32; source: (M, N)
-    float32 or bfloat16, packed, possibly `out` itself.  out_dtype: "bf16" or "f32", or that of
+    float32 or bfloat16, packed, possibly `out` itself (but not otherwise overlapping it).  out_dtype: "bf16" or "f32", or that of
     `out`, which is written where it is given.  Sums are float32, rounded once; for a bfloat16 C of
     more than 32 rows the matrix instructions keep 13 binary places of eight neighbouring products
     below the largest (1.5e-5 of C on normal data), for a float32 C 24."""

@@ -64,7 +64,8 @@ typedef struct {
 
 int gemm_block_workspace(const gemm_block_desc *desc, size_t *bytes);
 
-/* A, B 16-byte aligned; bias (N floats) and source (M x N, packed rows; may be C) or NULL. */
+/* A, B 16-byte aligned; bias (N floats) and source (M x N, packed rows) or NULL.  The source may be C itself
+ * if it has C's type; where it, or the bias, overlaps C otherwise: GEMM_ERR_INVALID_ARG. */
 int gemm_block_run(const gemm_block_desc *desc, const void *A, const float *scale_a,
                    const void *B, const float *scale_b, void *C, const float *bias,
                    const void *source, void *workspace, size_t workspace_bytes, void *stream);

@@ -24,3 +24,19 @@ def test_clip_of_a_gradient_that_is_there_twice(dev):
     norm = dg.clip_grad_norm([g, g], 1e-2, out=[one, two])
     assert torch.equal(one, two) and torch.equal(norm, dg.grad_norm([g, g]))
     assert abs(float(one.double().norm()) * 2 ** 0.5 - 1e-2) < 1e-5
+
+
+def test_product_into_a_part_of_its_source(dev):
+    g = gen(52)
+    a, b = (dg.block_quantize(randn(g, n, 300).to(dev)) for n in (40, 24))
+    held = randn(g, 41, 24).to(dev)
+    before = held.clone()
+    narrow = held.view(torch.bfloat16)[:20].view(40, 24)
+    for kw in (dict(source=held[:40], out=held[1:]), dict(source=held[:40], out=narrow),
+               dict(bias_col=held[3], out=held[:40])):
+        with pytest.raises(ValueError, match="overlaps"):
+            dg.block_gemm(a, b, **kw)
+    assert torch.equal(held, before)
+    want = dg.block_gemm(a, b, out_dtype="f32", source=before[1:])
+    assert torch.equal(dg.block_gemm(a, b, source=held[1:], out=held[1:]), want)
+    assert torch.equal(held[0], before[0])

@@ -115,3 +115,27 @@ def test_norm_backward_overlaps_against_plain_sets():
             assert got == (L.GEMM_ERR_WORKSPACE if want else L.GEMM_ERR_INVALID_ARG), (rows, cols, stride, at)
             got = back(P + at * es, P, stride, far, cols, rows, cols, dtype)
             assert got == (L.GEMM_ERR_WORKSPACE if want else L.GEMM_ERR_INVALID_ARG), (rows, cols, stride, at)
+
+
+def product(C, source=None, bias=None, M=100, N=90, dtype_c=L.GEMM_F32, dtype_source=L.GEMM_F32):
+    """Status of a product that needs a workspace and has none."""
+    far = P << 8
+    d = O.GemmBlockDesc(M=M, N=N, K=9000, lda=9008, ldb=9008, scale_lda=M, scale_ldb=N, dtype_c=dtype_c,
+                        dtype_source=dtype_source)
+    return O.load().gemm_block_run(d, far, far, far, far, C, bias, source, None, 0, None)
+
+
+def test_product_refuses_a_source_or_bias_that_overlaps_c():
+    inv, ok, bf16 = L.GEMM_ERR_INVALID_ARG, L.GEMM_ERR_WORKSPACE, L.GEMM_BF16
+    all_f32 = 100 * 90 * 4
+    for kw, want in ((dict(source=P), ok), (dict(source=P, dtype_c=bf16, dtype_source=bf16), ok),
+                     (dict(source=P, dtype_c=bf16), inv), (dict(source=P, dtype_source=bf16), inv),
+                     (dict(source=P + 4), inv), (dict(source=P - 360), inv),
+                     (dict(source=P + all_f32), ok), (dict(source=P - all_f32), ok),
+                     (dict(source=P + all_f32 - 4), inv), (dict(source=P - all_f32 + 4), inv),
+                     (dict(source=P + all_f32 // 2, dtype_c=bf16), ok),
+                     (dict(source=P - all_f32 // 2, dtype_source=bf16), ok),
+                     (dict(bias=P), inv), (dict(bias=P + 400), inv), (dict(bias=P - 360), ok),
+                     (dict(bias=P - 356), inv), (dict(bias=P + all_f32), ok),
+                     (dict(bias=P, M=1), ok), (dict(bias=P, M=1, dtype_c=bf16), inv)):
+        assert product(P, **kw) == want, kw

@@ -109,9 +109,9 @@ def block_quantize(x, block="row", transposed=False, pow2=False):
     transpose (cols, rows), "both" for the pair of them from one read of x."""
     if transposed not in (False, True, "both"):
         raise ValueError(f'transposed must be False, True or "both"; got {transposed!r}')
-    pow2 = bool(pow2)
+    both, pow2 = transposed == "both", bool(pow2)
     data, scales, data_t, scales_t = _binding().block_quantize(
-        x, block, transposed is not True, transposed is not False, pow2)
+        x, block, both or not transposed, both or bool(transposed), pow2)
     rows, cols = x.shape
     one = BlockScaled(data, scales, cols, block, pow2) if data is not None else None
     other = BlockScaled(data_t, scales_t, rows, block, pow2) if data_t is not None else None

@@ -374,7 +374,7 @@ PyObject *layer_norm_backward(PyObject *, PyObject *const *arg, Py_ssize_t) {
   });
 }
 
-struct Sequence {   // a list or tuple of Python objects, or what can be made one
+struct Sequence {   // a list or tuple of Python objects, or what can be made one (which may be read once)
   PyObject *fast;
   explicit Sequence(PyObject *o) : fast(PySequence_Fast(o, "a sequence of tensors is wanted")) {
     if (!fast) throw PythonError{};
@@ -397,7 +397,7 @@ PyObject *norm(PyObject *, PyObject *const *arg, Py_ssize_t) {
       if (!(max_norm >= 0.0)) throw Refused("max_norm must not be negative or NaN");
     }
     const bool into = arg[1] != Py_None;
-    const Sequence outs(into ? arg[1] : arg[0]);
+    const Sequence outs(into ? arg[1] : grads.fast);
     if (outs.size() != grads.size())
       throw Refused("out has " + std::to_string(outs.size()) + " tensors for " +
                     std::to_string(grads.size()) + " gradients");

@@ -35,3 +35,19 @@ def test_quantise_takes_truth_values_of_any_type(monkeypatch, transposed, sides)
 def test_quantise_refuses_other_sides(transposed):
     with pytest.raises(ValueError, match="transposed must be"):
         dg.block_quantize(torch.zeros(3, 5), transposed=transposed)
+
+
+def test_gradients_may_come_from_a_generator():
+    """A generator can be read once: it gets as far as a list does, to the check of its tensors."""
+    grads = [torch.zeros(3), torch.zeros(4)]
+    for call in (lambda g: dg.grad_norm(g), lambda g: dg.clip_grad_norm(g, 1.0),
+                 lambda g: dg.clip_grad_norm(g, 1.0, out=(t for t in grads))):
+        for given in (grads, tuple(grads), (t for t in grads), iter(grads)):
+            with pytest.raises(ValueError, match="gradient 0 is on cpu"):
+                call(given)
+    with pytest.raises(ValueError, match="out has 1 tensors for 2"):
+        dg.clip_grad_norm((t for t in grads), 1.0, out=(t for t in grads[:1]))
+    with pytest.raises(ValueError, match="the list of gradients is empty"):
+        dg.grad_norm(t for t in grads[:0])
+    with pytest.raises(TypeError, match="sequence of tensors"):
+        dg.grad_norm(3)

@@ -8,8 +8,6 @@ torch's, so the calls can be recorded into a HIP graph.  The checks and calls ar
 """
 import ctypes
 
-import torch
-
 from . import _lib
 
 GEMM_BLOCK_ROW, GEMM_BLOCK_TILE = 0, 1
@@ -94,6 +92,7 @@ class BlockScaled:
     @property
     def values(self):
         """The codes as torch's float8 values, (rows, K)."""
+        import torch
         return self.data.view(torch.float8_e4m3fn)[:, :self.K]
 
     def __repr__(self):

@@ -1,4 +1,8 @@
 """How the Python calls of the operators take their arguments (CPU: nothing here reaches a kernel)."""
+import os
+import subprocess
+import sys
+
 import pytest
 
 np = pytest.importorskip("numpy")
@@ -6,6 +10,8 @@ torch = pytest.importorskip("torch")
 
 import dense_gemm_design_amd as dg  # noqa: E402
 from dense_gemm_design_amd import ops as O  # noqa: E402
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 
 
 @pytest.mark.parametrize("transposed,sides", [(False, (True, False)), (True, (False, True)),
@@ -51,3 +57,12 @@ def test_gradients_may_come_from_a_generator():
         dg.grad_norm(t for t in grads[:0])
     with pytest.raises(TypeError, match="sequence of tensors"):
         dg.grad_norm(3)
+
+
+def test_the_package_imports_without_torch():
+    """Descriptors, constants and the build need no torch; what runs a kernel imports it by itself."""
+    code = ("import sys; sys.modules['torch'] = None; import dense_gemm_design_amd as dg; "
+            "print(dg.make_desc(256, 256, 256, dg.GEMM_BF16, dg.GEMM_F32).M, dg.BlockScaled.__name__)")
+    r = subprocess.run([sys.executable, "-c", code], cwd=ROOT, capture_output=True, text=True)
+    assert r.returncode == 0, r.stderr
+    assert r.stdout.split() == ["256", "BlockScaled"]

@@ -1,10 +1,12 @@
-"""Builds the HIP library libdgemm.so in-tree for gfx950 with hipcc, and the Python binding of the
-operators around the product, _binding.so, which calls it.
+"""Builds the HIP library libdgemm.so in-tree for gfx950 with hipcc, and, where torch is installed, the
+Python binding of the operators around the product, _binding.so, which calls it.
 
 Each translation unit compiles to an object of its own, all at once (the wide-wave kernels that
 read a source matrix sit in gemm_src_*.hip for this; the operators around the product in
 ops_*.hip), and the objects are linked into the shared library."""
+import importlib.util
 import os
+import shutil
 import subprocess
 import sys
 import tempfile
@@ -32,12 +34,13 @@ BINDING_LIB = os.path.join(HERE, "_binding.so")
 
 
 def binding_command(out):
-    """g++ on the Python binding of the operators (host code only), against torch's headers."""
+    """The host compiler (g++, or ROCm's) on the Python binding of the operators, against torch's headers."""
     import sysconfig
 
     import torch
     from torch.utils.cpp_extension import include_paths, library_paths
-    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall", "-fvisibility=hidden",
+    cxx = shutil.which("g++") or os.path.join(os.path.dirname(HIPCC), "amdclang++")
+    cmd = [cxx, "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall", "-fvisibility=hidden",
            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}"]
     cmd += [f for d in (*include_paths(), sysconfig.get_paths()["include"]) for f in ("-isystem", d)]
     cmd += ["-o", out, BINDING, f"-L{HERE}", "-l:libdgemm.so", "-Wl,-rpath,$ORIGIN"]
@@ -78,7 +81,10 @@ def build(verbose: bool = False, extra=()) -> str:
             print(" ".join(link), flush=True)
         subprocess.run(link, check=True)
     os.replace(LIB + ".tmp", LIB)
-    build_binding(verbose)
+    if importlib.util.find_spec("torch"):
+        build_binding(verbose)
+    else:   # the C library is whole; only the calls that take torch tensors need the binding
+        print("torch is not installed: _binding.so is not built", flush=True)
     return LIB
 
 

@@ -66,3 +66,35 @@ def test_the_package_imports_without_torch():
     r = subprocess.run([sys.executable, "-c", code], cwd=ROOT, capture_output=True, text=True)
     assert r.returncode == 0, r.stderr
     assert r.stdout.split() == ["256", "BlockScaled"]
+
+
+def recorded_build(monkeypatch, torch_there, gxx_there):
+    """The commands of a build, none of them run."""
+    from dense_gemm_design_amd import build as B
+    ran = []
+
+    class Done:
+        returncode = 0
+
+    monkeypatch.setattr(B.subprocess, "run", lambda c, **kw: ran.append(c) or Done())
+    monkeypatch.setattr(B.os, "replace", lambda a, b: None)
+    monkeypatch.setattr(B.shutil, "which", lambda name: "/usr/bin/" + name if gxx_there else None)
+    if not torch_there:
+        monkeypatch.setitem(sys.modules, "torch", None)
+    assert B.build() == B.LIB
+    assert sum("-c" in c for c in ran) == len(B.SOURCES)
+    return ran[len(B.SOURCES) + 1:]   # behind the library's link
+
+
+@pytest.mark.parametrize("gxx_there", [True, False])
+def test_the_library_builds_without_torch(monkeypatch, capsys, gxx_there):
+    """hipcc alone makes the C library; only the Python binding needs torch's headers."""
+    assert recorded_build(monkeypatch, False, gxx_there) == []
+    assert "torch" in capsys.readouterr().out
+
+
+@pytest.mark.parametrize("gxx_there", [True, False])
+def test_the_binding_builds_without_gxx(monkeypatch, gxx_there):
+    (cmd,) = recorded_build(monkeypatch, True, gxx_there)
+    assert os.path.basename(cmd[0]) == ("g++" if gxx_there else "amdclang++")
+    assert any(c.endswith("binding.cpp") for c in cmd)

@@ -96,6 +96,11 @@ void vector_of(const char *what, const at::Tensor &t, int64_t n, at::ScalarType 
                         (one == other ? "" : " or " + type_name(other)));
 }
 
+// A tensor that a call wrote into: autograd then refuses to use what it saved of it before.
+void written(const at::Tensor &t) {
+  if (!t.is_inference()) t.unsafeGetTensorImpl()->bump_version();
+}
+
 at::Tensor make(const at::Tensor &like, at::IntArrayRef sizes, at::ScalarType t) {
   return at::empty(sizes, like.options().dtype(t).requires_grad(false));
 }
@@ -278,7 +283,8 @@ PyObject *block_gemm(PyObject *, PyObject *const *arg, Py_ssize_t) {
     on("bias_col", bias);
     on("source", source);
     on("out", out);
-    if (!out.defined()) out = make(a.data, {M, N}, arg[8] == Py_True ? at::kFloat : at::kBFloat16);
+    const bool given = out.defined();
+    if (!given) out = make(a.data, {M, N}, arg[8] == Py_True ? at::kFloat : at::kBFloat16);
     if (M && N) {
       gemm_block_desc d{};
       d.M = M;
@@ -304,6 +310,7 @@ PyObject *block_gemm(PyObject *, PyObject *const *arg, Py_ssize_t) {
         throw Refused("out overlaps source, or bias_col, and is not the source itself");
       ok(st, "gemm_block_run");
     }
+    if (given) written(out);
     PyObject *r = THPVariable_Wrap(out);
     if (!r) throw PythonError{};
     return r;
@@ -448,6 +455,7 @@ PyObject *norm(PyObject *, PyObject *const *arg, Py_ssize_t) {
       if (st == GEMM_ERR_INVALID_ARG)   // what else is invalid has been refused above
         throw Refused("what is written for one gradient overlaps another one, or its output");
       ok(st, "gemm_clip_grad_norm");
+      for (Py_ssize_t i = 0; i < outs.size(); ++i) written(THPVariable_Unpack(outs[i]));
     } else {
       ok(gemm_grad_norm(list.data(), count, (float *)out.data_ptr(), w.ptr, w.bytes, s.ptr),
          "gemm_grad_norm");

@@ -3,7 +3,10 @@ gradients, and the clipping of a list of gradients (C ABI in include/gemm_ops.h)
 
 Every function takes torch tensors on one GPU, checks them (ValueError) before anything is
 launched, and enqueues kernels on torch's current stream of that GPU; outputs and workspaces are
-torch's, so the calls can be recorded into a HIP graph.  The checks and calls are compiled
+torch's, so the calls can be recorded into a HIP graph.  They are plain kernels to autograd: results
+carry no history, whether or not the arguments require gradients, so a backward pass calls them by itself
+(in a torch.autograd.Function, or as examples/fp8_linear.py does); what is written in place or into
+`out` counts as changed, so autograd refuses to use what it had saved of it.  The checks and calls are compiled
 (csrc/binding.cpp); load() gives the C ABI itself through ctypes.
 """
 import ctypes

@@ -47,9 +47,19 @@ std::string type_name(at::ScalarType t) {
                 list_of(t.sizes()) + " with strides " + list_of(t.strides()));
 }
 
+// what the kernels read is the memory at data_ptr(), by strides
+bool plain(const at::Tensor &t) { return t.layout() == at::kStrided && !t.is_neg(); }
+[[noreturn]] void refuse_layout(const std::string &what, const at::Tensor &t) {
+  throw Refused(what + (t.layout() == at::kStrided
+                            ? " is a lazily negated view; pass what resolve_neg() gives"
+                            : " must be a strided tensor"));
+}
+
 const at::Tensor &tensor(const std::string &what, PyObject *o) {
   if (!THPVariable_Check(o)) throw Refused(what + " must be a torch tensor");
-  return THPVariable_Unpack(o);
+  const at::Tensor &t = THPVariable_Unpack(o);
+  if (!plain(t)) refuse_layout(what, t);
+  return t;
 }
 // None stands for an undefined tensor
 const at::Tensor &maybe(const char *what, PyObject *o) {
@@ -416,6 +426,7 @@ PyObject *norm(PyObject *, PyObject *const *arg, Py_ssize_t) {
         throw Refused("gradient " + std::to_string(i) + " must be a torch tensor");
       const at::Tensor &g = THPVariable_Unpack(grads[i]);
       const auto name = [&] { return "gradient " + std::to_string(i); };
+      if (!plain(g)) refuse_layout(name(), g);
       if (!is_type(g.scalar_type()) || !g.is_contiguous())
         refuse(name(), g, "packed float32 or bfloat16");
       if (!g.is_cuda() || (device >= 0 && g.get_device() != device)) {

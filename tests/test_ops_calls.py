@@ -98,3 +98,26 @@ def test_the_binding_builds_without_gxx(monkeypatch, gxx_there):
     (cmd,) = recorded_build(monkeypatch, True, gxx_there)
     assert os.path.basename(cmd[0]) == ("g++" if gxx_there else "amdclang++")
     assert any(c.endswith("binding.cpp") for c in cmd)
+
+
+def test_tensors_that_are_not_plain_memory_are_refused():
+    """A lazily negated view holds the other sign in memory; a sparse tensor holds no rows."""
+    x, w, m = torch.ones(40, 64), torch.ones(64), torch.ones(40)
+    neg = lambda t: torch._neg_view(t)   # noqa: E731 -- what .imag of a conjugate is
+    a = dg.BlockScaled(torch.zeros(40, 64, dtype=torch.uint8), torch.ones(1, 40).t(), 64, "row")
+    calls = (lambda: dg.block_quantize(neg(x)), lambda: dg.layer_norm(neg(x), w),
+             lambda: dg.layer_norm(x, neg(w)), lambda: dg.layer_norm(x, w, neg(w)),
+             lambda: dg.layer_norm_backward(neg(x), x, w, m, m),
+             lambda: dg.layer_norm_backward(x, x, w, neg(m), m), lambda: dg.grad_norm([neg(x)]),
+             lambda: dg.clip_grad_norm([neg(x), x], 1.0),
+             lambda: dg.block_gemm(a, a, source=neg(torch.ones(40, 40))),
+             lambda: dg.block_gemm(a, a, out=neg(torch.ones(40, 40))),
+             lambda: dg.block_gemm(dg.BlockScaled(a.data, neg(a.scales), 64, "row"), a))
+    for call in calls:
+        with pytest.raises(ValueError, match="negated"):
+            call()
+    sparse = torch.eye(40).to_sparse()
+    for call in (lambda: dg.block_quantize(sparse), lambda: dg.layer_norm(sparse, m),
+                 lambda: dg.grad_norm([sparse]), lambda: dg.block_gemm(a, a, source=sparse)):
+        with pytest.raises(ValueError, match="strided"):
+            call()

@@ -26,7 +26,7 @@ struct Status {                     // a gemm_status other than GEMM_OK
   const char *where;
 };
 
-PyObject *raw_stream, *gemm_error, *str_row, *str_tile;
+PyObject *raw_stream, *gemm_error, *out_of_memory, *str_row, *str_tile;
 
 std::string list_of(at::IntArrayRef v) {
   std::string s = "(";
@@ -190,6 +190,8 @@ PyObject *guarded(F &&body) {
       Py_DECREF(err);
     }
   } catch (const PythonError &) {
+  } catch (const c10::OutOfMemoryError &e) {
+    PyErr_SetString(out_of_memory, e.what_without_backtrace());
   } catch (const c10::Error &e) {
     PyErr_SetString(PyExc_RuntimeError, e.what_without_backtrace());
   } catch (const std::exception &e) {
@@ -512,8 +514,9 @@ PyObject *attribute(const char *from, const char *name) {
 PyMODINIT_FUNC PyInit__binding() {
   raw_stream = attribute("torch._C", "_cuda_getCurrentRawStream");
   gemm_error = raw_stream ? attribute("dense_gemm_design_amd._lib", "GemmError") : nullptr;
+  out_of_memory = gemm_error ? attribute("torch", "OutOfMemoryError") : nullptr;
   str_row = PyUnicode_InternFromString("row");
   str_tile = PyUnicode_InternFromString("tile");
-  if (!raw_stream || !gemm_error || !str_row || !str_tile) return nullptr;
+  if (!raw_stream || !gemm_error || !out_of_memory || !str_row || !str_tile) return nullptr;
   return PyModule_Create(&module);
 }

@@ -268,7 +268,8 @@ bool packed(const at::Tensor &t, int64_t M, int64_t N) {
          t.is_contiguous();
 }
 
-// (a.data, a.scales, a.block, b.data, b.scales, b.block, K, pow2, fp32 out, bias, source, out) -> C
+// (a.data, a.scales, a.block, b.data, b.scales, b.block, K, pow2, fp32 out, bias, source, out, exact)
+// -> C
 PyObject *block_gemm(PyObject *, PyObject *const *arg, Py_ssize_t) {
   return guarded([&] {
     const int64_t K = PyLong_AsLongLong(arg[6]);
@@ -310,6 +311,7 @@ PyObject *block_gemm(PyObject *, PyObject *const *arg, Py_ssize_t) {
       d.pow2 = arg[7] == Py_True;
       d.dtype_c = gemm_type(out.scalar_type());
       d.dtype_source = source.defined() ? gemm_type(source.scalar_type()) : GEMM_F32;
+      d.exact = arg[12] == Py_True;
       size_t need = 0;
       ok(gemm_block_workspace(&d, &need), "gemm_block_workspace");
       const Stream s(on.device);
@@ -488,7 +490,7 @@ PyObject *norm(PyObject *, PyObject *const *arg, Py_ssize_t) {
     return name(self, arg, n);                                                                 \
   }
 DG_CALL(block_quantize, 5)
-DG_CALL(block_gemm, 12)
+DG_CALL(block_gemm, 13)
 DG_CALL(layer_norm, 4)
 DG_CALL(layer_norm_backward, 5)
 DG_CALL(norm, 3)

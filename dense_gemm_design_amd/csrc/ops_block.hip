@@ -17,7 +17,8 @@
 //    where all scales are powers of two, gives it their exponents as operands and lets it
 //    accumulate by itself;
 //  * an fp32 C takes four 16 x 16 x 32 bf16 MFMAs a block, at half the rate, on the codes converted
-//    in registers, which is exact; so do products of few rows, which wait for memory anyway.
+//    in registers, which is exact; so does a bf16 C that the caller wants exact, and so do products of few
+//    rows, which wait for memory anyway.
 #include "../../include/gemm_ops.h"
 #include "ops_block.h"
 
@@ -484,7 +485,8 @@ BlockPlan plan_of(const gemm_block_desc &d) {
     if (splits > kb / 16) splits = kb / 16;
     return {PLAN_FEW, splits > 1 ? (int)splits : 1, 1, (int32_t)nt, 0};
   }
-  if (d.dtype_c == GEMM_BF16 && kb && d.N >= 4) {   // (the wide tiles' quads want four columns)
+  const bool bf16_mfma = d.dtype_c == GEMM_F32 || d.exact;
+  if (!bf16_mfma && kb && d.N >= 4) {   // (the wide tiles' quads want four columns)
     // Tiles of 256 x 256 (wide with powers of two, eight waves otherwise) or, for fp32 scales of 128 x
     // 128 blocks, wide ones of 192 x 256, whose round over the CUs takes 0.74 as long: 8192^3 542 us on
     // six rounds of them, 498 on four of 256; 4096 x 14336 x 4096 237 us on five, 263 on four.
@@ -498,7 +500,7 @@ BlockPlan plan_of(const gemm_block_desc &d) {
     if (mt * nt >= kCUs)
       return {d.pow2 || narrow ? PLAN_WIDE : PLAN_256, 1, (int32_t)mt, (int32_t)nt, (int32_t)(mt * nt)};
   }
-  // Tiles of 128 x 128 (an fp32 C's codes as bf16 leave no registers for larger sub-tiles).  Either
+  // Tiles of 128 x 128 (codes as bf16 leave no registers for larger sub-tiles).  Either
   // PLAN_128, two workgroups a CU, a tile each: a k-block takes c1 us for one of them alone, c2 for two.
   // Or PLAN_CUT, one of twice the waves a CU, which takes two k-blocks in c us, and a round of tiles
   // 1.5 us more, in which it only writes: as many tiles as fill rounds of all CUs are taken whole, and K
@@ -508,9 +510,9 @@ BlockPlan plan_of(const gemm_block_desc &d) {
   // 89 and 64, 49 for the two in the middle; powers of two: 69, 78 and 52, 43.)
   const int64_t mt = (d.M + kTile - 1) / kTile, nt = (d.N + kTile - 1) / kTile;
   const int64_t t = mt * nt, rest = t % kCUs;
-  const bool f32 = d.dtype_c == GEMM_F32;
-  const double c1 = f32 ? 1.3 : d.pow2 ? 0.75 : 0.9, c2 = f32 ? 2.1 : d.pow2 ? 1.05 : 1.27;
-  const double c = f32 ? 2.33 : d.pow2 ? 1.22 : 1.45;
+  const double c1 = bf16_mfma ? 1.3 : d.pow2 ? 0.75 : 0.9;
+  const double c2 = bf16_mfma ? 2.1 : d.pow2 ? 1.05 : 1.27;
+  const double c = bf16_mfma ? 2.33 : d.pow2 ? 1.22 : 1.45;
   const int64_t last = t % (2 * kCUs);
   const double pairs =
       (double)kb * ((double)(t / (2 * kCUs)) * c2 + (last > kCUs ? c2 : last ? c1 : 0.0));
@@ -541,7 +543,7 @@ void launch_tiles(const BlockArgs &a, bool rowb, hipStream_t s) {
 }
 template <int KG>
 void launch_small(const BlockArgs &a, bool rowb, const gemm_block_desc &d, hipStream_t s) {
-  if (d.dtype_c == GEMM_F32)
+  if (d.dtype_c == GEMM_F32 || d.exact)
     launch_tiles<kTile, kTile, 2, 2, KG, MODE_EXACT>(a, rowb, s);
   else if (d.pow2)
     launch_tiles<kTile, kTile, 2, 2, KG, MODE_POW2>(a, rowb, s);

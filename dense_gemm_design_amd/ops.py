@@ -24,7 +24,8 @@ class GemmBlockDesc(ctypes.Structure):
                 ("lda", ctypes.c_int64), ("ldb", ctypes.c_int64),
                 ("scale_lda", ctypes.c_int64), ("scale_ldb", ctypes.c_int64),
                 ("block_b", ctypes.c_int32), ("pow2", ctypes.c_int32),
-                ("dtype_c", ctypes.c_int32), ("dtype_source", ctypes.c_int32)]
+                ("dtype_c", ctypes.c_int32), ("dtype_source", ctypes.c_int32),
+                ("exact", ctypes.c_int32)]
 
 
 class GemmTensor(ctypes.Structure):
@@ -120,13 +121,15 @@ def block_quantize(x, block="row", transposed=False, pow2=False):
     return (one, other) if one and other else one or other
 
 
-def block_gemm(a, b, out_dtype="bf16", bias_col=None, source=None, out=None):
+def block_gemm(a, b, out_dtype="bf16", bias_col=None, source=None, out=None, exact=False):
     """C (M, N) = A B^T + bias_col + source of BlockScaled operands a (M, K), scaled per row and
     block of 128, and b (N, K), scaled per row or per tile.  bias_col: N float32; source: (M, N)
     float32 or bfloat16, packed, possibly `out` itself (but not otherwise overlapping it).  out_dtype: "bf16" or "f32", or that of
     `out`, which is written where it is given.  Sums are float32, rounded once; for a bfloat16 C of
     more than 32 rows the matrix instructions keep 13 binary places of eight neighbouring products
-    below the largest (1.5e-5 of C on normal data), for a float32 C 24."""
+    below the largest (1.5e-5 of C on normal data), for a float32 C 24.  exact: 24 for a bfloat16 C of
+    any number of rows too, at about half the speed -- for sums whose terms cancel, and where a row is to have
+    the places that it has in a smaller batch."""
     for what, q in (("a", a), ("b", b)):
         if not isinstance(q, BlockScaled):
             raise ValueError(f"{what} must be a BlockScaled")
@@ -135,7 +138,8 @@ def block_gemm(a, b, out_dtype="bf16", bias_col=None, source=None, out=None):
     if out is None and out_dtype not in ("bf16", "f32"):
         raise ValueError(f'out_dtype must be "bf16" or "f32"; got {out_dtype!r}')
     return _binding().block_gemm(a.data, a.scales, a.block, b.data, b.scales, b.block, a.K,
-                                 bool(a.pow2 and b.pow2), out_dtype == "f32", bias_col, source, out)
+                                 bool(a.pow2 and b.pow2), out_dtype == "f32", bias_col, source, out,
+                                 bool(exact))
 
 
 # ---- layer norm -------------------------------------------------------------------------------

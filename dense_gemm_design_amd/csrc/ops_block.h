@@ -66,7 +66,7 @@ __device__ __forceinline__ void store_four(const BlockArgs &a, int64_t m, int64_
 
 // The same in three steps, for kernels whose threads have many outputs: the extras are loaded for several
 // of them before the first is used (one after the other, each waited for a trip to memory: 8026 x
-// 5184 x 192 with an fp32 source took 157 us, 74 so).  N >= 4; what lies past M or N is loaded from inside,
+// 5184 x 192 with an fp32 source took 157 us, 74 to 79 so).  N >= 4; what lies past M or N is loaded from inside,
 // a quad that N ends in from the row's last four.
 __device__ __forceinline__ int64_t quad_inside(const BlockArgs &a, int64_t n) {
   return n + 4 <= a.N ? n : a.N - 4;

@@ -477,7 +477,7 @@ BlockPlan plan_of(const gemm_block_desc &d) {
   const int64_t kb = (d.K + 127) / 128;
   if (d.M <= 32) {
     // 32 columns a workgroup where there are more rows of A to read beside them than one block's and
-    // columns enough (32 x 16384 x 16384 69 us, 97 on 16; 32 x 4096 x 4096 10.8, 8.8); K in pieces where
+    // columns enough (32 x 16384 x 16384 79 us, 103 on 16; 32 x 4096 x 4096 11.7, 9.5); K in pieces where
     // there are few columns and much of it
     const int cols = few_columns(d);
     const int64_t nt = (d.N + cols - 1) / cols;
@@ -488,8 +488,9 @@ BlockPlan plan_of(const gemm_block_desc &d) {
   const bool bf16_mfma = d.dtype_c == GEMM_F32 || d.exact;
   if (!bf16_mfma && kb && d.N >= 4) {   // (the wide tiles' quads want four columns)
     // Tiles of 256 x 256 (wide with powers of two, eight waves otherwise) or, for fp32 scales of 128 x
-    // 128 blocks, wide ones of 192 x 256, whose round over the CUs takes 0.74 as long: 8192^3 542 us on
-    // six rounds of them, 498 on four of 256; 4096 x 14336 x 4096 237 us on five, 263 on four.
+    // 128 blocks, wide ones of 192 x 256, whose round over the CUs takes 0.74 as long: 8192^3 560 us on
+    // six rounds of them, 514 on four of 256; 4096 x 14336 x 4096 236 us on five, 271 on four.  (0.62 to 0.73
+    // over eleven shapes: 2048 x 16384 x 4096 takes 151 us by this rule, 142 on the other side.)
     const auto rounds = [&](int rows) {
       return (((d.M + rows - 1) / rows) * ((d.N + 255) / 256) + kCUs - 1) / kCUs;
     };
@@ -505,9 +506,9 @@ BlockPlan plan_of(const gemm_block_desc &d) {
   // Or PLAN_CUT, one of twice the waves a CU, which takes two k-blocks in c us, and a round of tiles
   // 1.5 us more, in which it only writes: as many tiles as fill rounds of all CUs are taken whole, and K
   // is cut for the rest, which costs 8 bytes an element and piece to write and read, and a launch.  What
-  // is less by this estimate.  (us on PLAN_128 and PLAN_CUT, fp32: 4096 x 14336 x 4096 481, 533; 2048 x
-  // 4096 x 8192 136, 143; 2048 x 2048 x 8192 86, 78; 1000 x 4104 x 8201 136, 93.  bf16, fp32 scales: 80,
-  // 89 and 64, 49 for the two in the middle; powers of two: 69, 78 and 52, 43.)
+  // is less by this estimate.  (us on PLAN_128 and PLAN_CUT, fp32: 4096 x 14336 x 4096 448, 506; 2048 x
+  // 4096 x 8192 130, 135; 2048 x 2048 x 8192 79, 67; 1000 x 4104 x 8201 133, 90.  bf16, fp32 scales: 77,
+  // 90 and 56, 47 for the two in the middle; powers of two: 66, 80 and 48, 39.)
   const int64_t mt = (d.M + kTile - 1) / kTile, nt = (d.N + kTile - 1) / kTile;
   const int64_t t = mt * nt, rest = t % kCUs;
   const double c1 = bf16_mfma ? 1.3 : d.pow2 ? 0.75 : 0.9;

@@ -13,8 +13,11 @@
 //    registers, so there the 192 accumulators have to be, and the fragments go to the accumulation
 //    registers.  A wave's columns are one block of B, whose power of two the MFMA applies; what is left of
 //    that scale, times A's, is one a row.  An MFMA's four results are added two slots later, when they
-//    have left the matrix unit.  4096 x 14336 x 4096 in 250 to 270 us by the card, 1.8 to 1.9 PFLOP/s
-//    (4 % less time with the scales' product formed first, which left the range of fp32 where C does not).
+//    have left the matrix unit.  4096 x 14336 x 4096 with a bias in 247 us between other launches, 1.95
+//    PFLOP/s, and 265 one after the other (4 % less with the scales' product formed first, which left the
+//    range of fp32 where C does not).  The matrix units are busy 0.44 of the time, a wave issues for 0.58,
+//    waits to issue for 0.16 and for memory, LDS or the barrier for 0.17: none of them fills it, and the time
+//    is near the sum of the MFMAs' and the additions', as if they overlapped little.  Why is not known.
 // Workgroups stay for tile after tile: the loads of the next one are under way when a tile ends, and
 // what a tile leaves in the registers is written out beside the next one's first step (written at
 // once by all CUs, the 33 MB of a round took 8 us in which nothing was multiplied).

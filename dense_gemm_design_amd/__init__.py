@@ -2,8 +2,9 @@
 
 The compute path is the HIP library libdgemm.so (csrc/, C ABI in include/gemm.h); this package
 is its Python binding.  See gemm() for a one-call helper on torch tensors, and ops.py for the
-operators around the product: block-scaled e4m3 operands (block_quantize, BlockScaled, block_gemm),
-layer norm and its gradients, and gradient clipping.
+operators around the product: block-scaled e4m3 operands (block_quantize, BlockScaled, block_gemm), int8
+operands with a scale a row (int8_quantize, Int8Scaled, int8_gemm), layer norm and its gradients, gradient
+clipping, and the AdamW step of a list of parameters (adamw_state, AdamWState, adamw_step).
 """
 from . import _lib
 from ._lib import (GemmDesc, GemmError, Plan, make_desc, load,  # noqa: F401
@@ -16,8 +17,9 @@ from ._lib import (GemmDesc, GemmError, Plan, make_desc, load,  # noqa: F401
                    GEMM_EPI_BIAS_ROW, GEMM_EPI_BIAS_COL, GEMM_EPI_RELU, GEMM_EPI_GELU,
                    GEMM_EPI_SILU, GEMM_EPI_AMAX, GEMM_EPI_SOURCE_F32, GEMM_EPI_SOURCE_BF16,
                    GemmEpilogueArgs)
-from .ops import (BlockScaled, block_gemm, block_quantize, clip_grad_norm,  # noqa: F401
-                  grad_norm, layer_norm, layer_norm_backward)
+from .ops import (AdamWState, BlockScaled, Int8Scaled, adamw_state, adamw_step,  # noqa: F401
+                  block_gemm, block_quantize, clip_grad_norm, grad_norm, int8_gemm, int8_quantize,
+                  layer_norm, layer_norm_backward)
 
 KERNEL_NAMES = {0: "cooperative", 1: "ping-pong", 3: "wide-wave"}  # gemm_plan_info.kernel
 MAPPINGS = {"linear_n": GEMM_MAP_LINEAR_N, "linear_m": GEMM_MAP_LINEAR_M,

@@ -331,6 +331,104 @@ PyObject *block_gemm(PyObject *, PyObject *const *arg, Py_ssize_t) {
   });
 }
 
+// (x, rows side, columns side) -> (codes, scales, codes_t, scales_t), None where not asked for
+PyObject *int8_quantize(PyObject *, PyObject *const *arg, Py_ssize_t) {
+  return guarded([&] {
+    const at::Tensor &x = tensor("x", arg[0]);
+    const Rows r = rows_of("x", x);
+    On on;
+    on("x", x);
+    at::Tensor out[4];
+    for (int side = 0; side < 2; ++side) {
+      if (arg[1 + side] != Py_True) continue;
+      const int64_t rows = side ? r.cols : r.rows, cols = side ? r.rows : r.cols;
+      out[2 * side] = make(x, {rows, up(cols, 16) * 16}, at::kChar);
+      out[2 * side + 1] = make(x, {rows}, at::kFloat);
+      if (cols == 0) out[2 * side + 1].fill_(0x1p-120);   // rows of nothing: the smallest scale
+    }
+    if (r.rows && r.cols) {
+      size_t need = 0;
+      ok(gemm_int8_quantize_workspace(r.rows, r.cols, out[0].defined(), out[2].defined(), &need),
+         "gemm_int8_quantize_workspace");
+      const Stream s(on.device);
+      const Workspace w(x, need);
+      const auto pitch = [&](int i) { return out[i].defined() ? out[i].size(1) : 0; };
+      ok(gemm_int8_quantize(x.data_ptr(), gemm_type(x.scalar_type()), r.rows, r.cols, r.stride,
+                            data(out[0]), pitch(0), (float *)data(out[1]), data(out[2]), pitch(2),
+                            (float *)data(out[3]), w.ptr, w.bytes, s.ptr),
+         "gemm_int8_quantize");
+    }
+    return tuple_of({out[0], out[1], out[2], out[3]});
+  });
+}
+
+// (a.data, a.scales, b.data, b.scales, K, fp32 out, bias, source, out) -> C
+PyObject *int8_gemm(PyObject *, PyObject *const *arg, Py_ssize_t) {
+  return guarded([&] {
+    const int64_t K = PyLong_AsLongLong(arg[4]);
+    if (K < 0) {
+      if (PyErr_Occurred()) throw PythonError{};
+      throw Refused("K must not be negative");
+    }
+    On on;
+    at::Tensor codes[2], scales[2];
+    int64_t pitch[2];
+    const int64_t width = up(K, 16) * 16;
+    for (int k = 0; k < 2; ++k) {
+      const std::string what = k ? "b" : "a";
+      codes[k] = tensor(what + ".data", arg[2 * k]);
+      scales[k] = tensor(what + ".scales", arg[2 * k + 1]);
+      const at::Tensor &d = codes[k], &sc = scales[k];
+      if (d.dim() != 2 || d.scalar_type() != at::kChar || d.size(1) != width)
+        refuse(what + ".data", d, "int8 codes (rows, " + std::to_string(width) + ")");
+      pitch[k] = d.size(0) > 1 && width ? d.stride(0) : width;
+      if ((width > 1 && d.stride(1) != 1) || pitch[k] < width || pitch[k] % 16)
+        refuse(what + ".data", d, "packed rows at multiples of 16 bytes");
+      vector_of((what + ".scales").c_str(), sc, d.size(0), at::kFloat, at::kFloat);
+      on(what, d);
+      on(what + ".scales", sc);
+    }
+    const int64_t M = codes[0].size(0), N = codes[1].size(0);
+    const at::Tensor &bias = maybe("bias_col", arg[6]), &source = maybe("source", arg[7]);
+    at::Tensor out = maybe("out", arg[8]);
+    const std::string shape =
+        "a packed float32 or bfloat16 matrix (" + std::to_string(M) + ", " + std::to_string(N) + ")";
+    if (out.defined() && !packed(out, M, N)) refuse("out", out, shape);
+    if (bias.defined()) vector_of("bias_col", bias, N, at::kFloat, at::kFloat);
+    if (source.defined() && !packed(source, M, N)) refuse("source", source, shape);
+    on("bias_col", bias);
+    on("source", source);
+    on("out", out);
+    const bool given = out.defined();
+    if (!given) out = make(codes[0], {M, N}, arg[5] == Py_True ? at::kFloat : at::kBFloat16);
+    if (M && N) {
+      gemm_int8_desc d{};
+      d.M = M;
+      d.N = N;
+      d.K = K;
+      d.lda = pitch[0];
+      d.ldb = pitch[1];
+      d.dtype_c = gemm_type(out.scalar_type());
+      d.dtype_source = source.defined() ? gemm_type(source.scalar_type()) : GEMM_F32;
+      size_t need = 0;
+      ok(gemm_int8_workspace(&d, &need), "gemm_int8_workspace");
+      const Stream s(on.device);
+      const Workspace w(codes[0], need);
+      const int st = gemm_int8_run(&d, codes[0].data_ptr(), (const float *)scales[0].data_ptr(),
+                                   codes[1].data_ptr(), (const float *)scales[1].data_ptr(),
+                                   out.data_ptr(), (const float *)data(bias), data(source), w.ptr,
+                                   w.bytes, s.ptr);
+      if (st == GEMM_ERR_INVALID_ARG)   // what else is invalid has been refused above
+        throw Refused("out overlaps an operand, bias_col, or a source that is not out itself");
+      ok(st, "gemm_int8_run");
+    }
+    if (given) written(out);
+    PyObject *r = THPVariable_Wrap(out);
+    if (!r) throw PythonError{};
+    return r;
+  });
+}
+
 // (x, weight, bias, eps) -> (y, mean, rstd)
 PyObject *layer_norm(PyObject *, PyObject *const *arg, Py_ssize_t) {
   return guarded([&] {
@@ -481,6 +579,138 @@ PyObject *norm(PyObject *, PyObject *const *arg, Py_ssize_t) {
   });
 }
 
+double real(const char *what, PyObject *o) {
+  const double v = PyFloat_AsDouble(o);
+  if (v == -1.0 && PyErr_Occurred()) throw PythonError{};
+  if (!(v - v == 0.0)) throw Refused(std::string(what) + " must be a finite number");
+  return v;
+}
+// One element of a type in device memory, or an undefined tensor if o is no tensor.
+const at::Tensor &held(const char *what, PyObject *o, at::ScalarType type, On &on) {
+  static const at::Tensor none;
+  if (!THPVariable_Check(o)) return none;
+  const at::Tensor &t = tensor(what, o);
+  if (t.scalar_type() != type || t.numel() != 1)
+    refuse(what, t, std::string(type == at::kLong ? "an int64" : "a float32") +
+                        " tensor of one element, or a number");
+  on(what, t);
+  return t;
+}
+
+// (params, grads, m, v, m_scales, v_scales, step, lr, beta1, beta2, eps, weight_decay, norm, max_norm,
+// copies) -> None
+PyObject *adamw_step(PyObject *, PyObject *const *arg, Py_ssize_t) {
+  return guarded([&] {
+    const Sequence params(arg[0]), grads(arg[1]);
+    const bool copying = arg[14] != Py_None;
+    const Sequence copies(copying ? arg[14] : params.fast);
+    if (params.size() == 0) throw Refused("the list of parameters is empty");
+    if (grads.size() != params.size() || copies.size() != params.size())
+      throw Refused("there are " + std::to_string(grads.size()) + " gradients" +
+                    (copying ? " and " + std::to_string(copies.size()) + " copies" : "") + " for " +
+                    std::to_string(params.size()) + " parameters");
+    On on;
+    std::vector<gemm_adamw_tensor> list((size_t)params.size());
+    int64_t blocks = 0;
+    const auto here = [&](const std::string &name, const at::Tensor &t) {
+      if (!t.is_cuda() || (on.device >= 0 && t.get_device() != on.device)) on(name, t);
+      on.device = t.get_device();
+    };
+    for (Py_ssize_t i = 0; i < params.size(); ++i) {
+      const auto name = [&](const char *kind) { return kind + (" " + std::to_string(i)); };
+      for (PyObject *o : {params[i], grads[i]})
+        if (!THPVariable_Check(o))
+          throw Refused(name(o == params[i] ? "parameter" : "gradient") + " must be a torch tensor");
+      const at::Tensor &p = THPVariable_Unpack(params[i]), &g = THPVariable_Unpack(grads[i]);
+      if (!plain(p)) refuse_layout(name("parameter"), p);
+      if (!plain(g)) refuse_layout(name("gradient"), g);
+      if (!is_type(p.scalar_type()) || !p.is_contiguous())
+        refuse(name("parameter"), p, "packed float32 or bfloat16");
+      if (!is_type(g.scalar_type()) || !g.is_contiguous() || g.sizes() != p.sizes())
+        refuse(name("gradient"), g, "packed float32 or bfloat16 " + list_of(p.sizes()) +
+                                        " like its parameter");
+      here(name("parameter"), p);
+      here(name("gradient"), g);
+      gemm_adamw_tensor &t = list[(size_t)i];
+      t = gemm_adamw_tensor{p.data_ptr(), g.data_ptr(), nullptr, p.numel(),
+                            gemm_type(p.scalar_type()), gemm_type(g.scalar_type())};
+      blocks += up(t.numel, 128);
+      if (copying && copies[i] != Py_None) {
+        const at::Tensor &c = tensor(name("copy"), copies[i]);
+        if (c.scalar_type() != at::kBFloat16 || !c.is_contiguous() || c.sizes() != p.sizes())
+          refuse(name("copy"), c, "packed bfloat16 " + list_of(p.sizes()) + " like its parameter");
+        here(name("copy"), c);
+        t.copy = c.data_ptr();
+      }
+    }
+    gemm_adamw_desc d{};
+    at::Tensor state[4];
+    const char *const names[4] = {"state.m", "state.v", "state.m_scales", "state.v_scales"};
+    const bool e4m3 = arg[4] != Py_None || arg[5] != Py_None;
+    d.dtype_state = e4m3 ? GEMM_FP8_E4M3 : GEMM_F32;
+    for (int k = 0; k < (e4m3 ? 4 : 2); ++k) {
+      const at::Tensor &t = state[k] = tensor(names[k], arg[2 + k]);
+      const at::ScalarType type = t.scalar_type();
+      const bool codes = type == at::kByte || type == at::kFloat8_e4m3fn;
+      const int64_t n = k < 2 ? blocks * 128 : blocks;
+      if (t.dim() != 1 || t.size(0) != n || !t.is_contiguous() ||
+          (e4m3 && k < 2 ? !codes : type != at::kFloat))
+        refuse(names[k], t, std::string("a packed vector of ") + std::to_string(n) +
+                                (e4m3 && k < 2 ? ", float8_e4m3fn or uint8" : ", torch.float32") +
+                                ", as adamw_state gives");
+      here(names[k], t);
+    }
+    d.m = state[0].data_ptr();
+    d.v = state[1].data_ptr();
+    d.m_scales = (float *)data(state[2]);
+    d.v_scales = (float *)data(state[3]);
+    const at::Tensor &step = held("step", arg[6], at::kLong, on);
+    if (step.defined()) {
+      d.step_at = (const int64_t *)step.data_ptr();
+    } else {
+      d.step = PyLong_AsLongLong(arg[6]);
+      if (d.step == -1 && PyErr_Occurred()) throw PythonError{};
+      if (d.step < 1) throw Refused("step counts from 1; got " + std::to_string(d.step));
+    }
+    const at::Tensor &lr = held("lr", arg[7], at::kFloat, on);
+    if (lr.defined())
+      d.lr_at = (const float *)lr.data_ptr();
+    else
+      d.lr = real("lr", arg[7]);
+    d.beta1 = real("beta1", arg[8]);
+    d.beta2 = real("beta2", arg[9]);
+    for (double b : {d.beta1, d.beta2})
+      if (!(b >= 0.0 && b < 1.0)) throw Refused("betas must lie in [0, 1)");
+    d.eps = real("eps", arg[10]);
+    if (d.eps < 0.0) throw Refused("eps must not be negative");
+    d.weight_decay = real("weight_decay", arg[11]);
+    if ((arg[12] == Py_None) != (arg[13] == Py_None))
+      throw Refused("norm and max_norm go together");
+    if (arg[12] != Py_None) {
+      const at::Tensor &norm = held("norm", arg[12], at::kFloat, on);
+      if (!norm.defined()) throw Refused("norm must be a torch tensor, as grad_norm gives");
+      d.norm = (const float *)norm.data_ptr();
+      d.max_norm = PyFloat_AsDouble(arg[13]);
+      if (d.max_norm == -1.0 && PyErr_Occurred()) throw PythonError{};
+      if (!(d.max_norm >= 0.0)) throw Refused("max_norm must not be negative or NaN");
+    }
+    {
+      const Stream s(on.device);
+      const int st = gemm_adamw_step(list.data(), params.size(), &d, s.ptr);
+      if (st == GEMM_ERR_INVALID_ARG)   // what else is invalid has been refused above
+        throw Refused("something that is written (a parameter, a copy, the state) overlaps something else");
+      ok(st, "gemm_adamw_step");
+    }
+    for (Py_ssize_t i = 0; i < params.size(); ++i) {
+      written(THPVariable_Unpack(params[i]));
+      if (list[(size_t)i].copy) written(THPVariable_Unpack(copies[i]));
+    }
+    for (const at::Tensor &t : state)
+      if (t.defined()) written(t);
+    Py_RETURN_NONE;
+  });
+}
+
 #define DG_CALL(name, count)                                                                   \
   PyObject *call_##name(PyObject *self, PyObject *const *arg, Py_ssize_t n) {                  \
     if (n != count) {                                                                          \
@@ -494,11 +724,15 @@ DG_CALL(block_gemm, 13)
 DG_CALL(layer_norm, 4)
 DG_CALL(layer_norm_backward, 5)
 DG_CALL(norm, 3)
+DG_CALL(int8_quantize, 3)
+DG_CALL(int8_gemm, 9)
+DG_CALL(adamw_step, 15)
 #undef DG_CALL
 
 #define DG_METHOD(name) {#name, (PyCFunction)(void (*)(void))call_##name, METH_FASTCALL, nullptr}
 PyMethodDef methods[] = {DG_METHOD(block_quantize), DG_METHOD(block_gemm), DG_METHOD(layer_norm),
                          DG_METHOD(layer_norm_backward), DG_METHOD(norm),
+                         DG_METHOD(int8_quantize), DG_METHOD(int8_gemm), DG_METHOD(adamw_step),
                          {nullptr, nullptr, 0, nullptr}};
 #undef DG_METHOD
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_binding", nullptr, -1, methods,

@@ -17,10 +17,7 @@
 // Bound by memory: the list read twice and written once.
 #include "../../include/gemm_ops.h"
 #include "ops_common.h"
-
-#include <stdlib.h>
-
-#include <algorithm>
+#include "ops_spans.h"
 
 namespace dg {
 namespace {
@@ -228,60 +225,18 @@ int check(const gemm_tensor *list, int64_t count, bool out) {
   return GEMM_OK;
 }
 
-struct Span {
-  uintptr_t begin, end;
-  bool written;
-};
-// The bytes of entry i: its data and its output, or one span where they are the same.  How many.
-int spans_of(const gemm_tensor &t, Span (&s)[2]) {
-  if (t.numel == 0) return 0;
-  const uintptr_t bytes = (uintptr_t)t.numel * (t.dtype == GEMM_F32 ? 4 : 2);
-  s[0] = Span{(uintptr_t)t.out, (uintptr_t)t.out + bytes, true};
-  s[1] = Span{(uintptr_t)t.data, (uintptr_t)t.data + bytes, false};
-  return t.out == t.data ? 1 : 2;
-}
-
 // GEMM_OK where no output overlaps another output, or data that are not exactly its own: workgroups
 // scale what they share in any order, so parts of it would be scaled twice.
 int check_apart(const gemm_tensor *list, int64_t count) {
-  // Most lists are cut from a few buffers, or allocated in order: a few runs of rising addresses that lie
-  // apart as wholes (0.7 us for 153 tensors into others, 5 to sort them).
-  constexpr int RUNS = 8;
-  constexpr uintptr_t NEAR = 512;   // an allocator's rounding
-  Span run[RUNS], s[2];
-  int runs = 0;
-  bool simple = true;
-  for (int64_t i = 0; i < count && simple; ++i)
-    for (int k = spans_of(list[i], s) - 1; k >= 0 && simple; --k) {
-      int to = 0;   // a run that ends just before it
-      while (to < runs && s[k].begin - run[to].end >= NEAR) ++to;
-      if (to < runs)
-        run[to].end = s[k].end;
-      else if (runs < RUNS)
-        run[runs++] = s[k];
-      else
-        simple = false;
-    }
-  const auto before = [](const Span &a, const Span &b) { return a.begin < b.begin; };
-  std::sort(run, run + runs, before);
-  for (int r = 1; r < runs; ++r) simple = simple && run[r - 1].end <= run[r].begin;
-  if (simple) return GEMM_OK;
-
-  Span *const all = (Span *)malloc((size_t)count * 2 * sizeof(Span));
-  if (!all) return GEMM_ERR_UNSUPPORTED;
-  int64_t n = 0;
-  for (int64_t i = 0; i < count; ++i)
-    for (int k = spans_of(list[i], s) - 1; k >= 0; --k) all[n++] = s[k];
-  std::sort(all, all + n, before);
-  uintptr_t read = 0, written = 0;   // where those so far end
-  bool apart = true;
-  for (int64_t i = 0; i < n; ++i) {
-    apart = apart && all[i].begin >= written && !(all[i].written && all[i].begin < read);
-    uintptr_t &end = all[i].written ? written : read;
-    end = std::max(end, all[i].end);
-  }
-  free(all);
-  return apart ? GEMM_OK : GEMM_ERR_INVALID_ARG;
+  return spans_apart<2>(count, [list](int64_t i, Span (&s)[2]) {
+    // its data and its output, or one span where they are the same
+    const gemm_tensor &t = list[i];
+    if (t.numel == 0) return 0;
+    const uintptr_t bytes = (uintptr_t)t.numel * (t.dtype == GEMM_F32 ? 4 : 2);
+    s[0] = Span{(uintptr_t)t.out, (uintptr_t)t.out + bytes, true};
+    s[1] = Span{(uintptr_t)t.data, (uintptr_t)t.data + bytes, false};
+    return t.out == t.data ? 1 : 2;
+  });
 }
 
 // The size of chunk that gives a list at least kGroups of them, within its bounds.

@@ -1,0 +1,432 @@
+// Quantisation to int8 with one fp32 scale a row (gemm_int8_quantize), of x, of its transpose (a scale
+// a column of x), or of both:
+//
+//   s = max(amax / 127, 2^-120),  q = the exact quotient x / s rounded to even
+//
+// Rounding: t = x r + 1.5 2^23 with r near 1 / s leaves the integer next to x / s in t's last bits, and
+// rest = x - q s is exact in fp32 (a multiple of the smaller of x's and s's last places, at most s / 2
+// and a little in size), so |rest| against s / 2 says whether q is the nearest integer, and where it is a
+// tie.  Four instructions a value; what is not right yet, one in some thousands, is mended behind a
+// branch.  (2^-120 as the smallest scale keeps every rest a normal multiple of 2^-149.)
+//
+//  * Rows alone: one pass, a row in the registers of a wave, of four or of sixteen.
+//  * With columns, or rows of over 65536: a first kernel leaves maxima of rows and columns over parts of
+//    x, at most 16 of a row and some 64 of a column; the second one's workgroups, 128 x 128 elements
+//    each, take the largest of their rows' and columns' parts themselves.  It reads x again, from the
+//    memory-side cache of 256 MB where x fits.
+//
+// Bound by memory.
+#include "../../include/gemm_ops.h"
+#include "ops_common.h"
+
+#include <algorithm>
+
+namespace dg {
+namespace {
+
+struct RowQuantArgs {
+  const void *x;
+  int64_t rows, cols, stride;
+  uint8_t *codes, *codes_t;
+  float *scales, *scales_t;
+  int64_t pitch, pitch_t;
+  uint32_t *row_parts, *col_parts;   // [part][rows], [part][cols]: bits of largest magnitudes
+  int32_t parts_r, parts_c;
+  int32_t wide, high;                // of a part: blocks of 128 columns, and rows
+  int32_t col_tiles;
+};
+
+// Largest over the 16 lanes of a DPP row, in each of them.
+__device__ __forceinline__ uint32_t row16_max(uint32_t v) {
+#define DG_ROR(n) \
+  v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x120 + n, 0xF, 0xF, false))
+  DG_ROR(8);
+  DG_ROR(4);
+  DG_ROR(2);
+  DG_ROR(1);
+#undef DG_ROR
+  return v;
+}
+
+// The scale of a row from the bits of its largest magnitude (NaN and infinity order above every number,
+// so they carry through the integer maxima).
+__device__ __forceinline__ float scale_of(uint32_t amax) {
+  if (amax >= 0x7F800000u) return float_of(0x7FC00000u);
+  return fmaxf(float_of(amax) / 127.0f, 0x1p-120f);
+}
+
+// Dividing by one scale.  All codes of a NaN scale are zeros.
+struct Divide {
+  float s, r, half;
+  uint32_t keep;
+  __device__ __forceinline__ explicit Divide(float scale) : s(scale) {
+    const bool fine = s == s;
+    r = fine ? __builtin_amdgcn_rcpf(s) : 0.0f;
+    half = 0.5f * s;
+    keep = fine ? ~0u : 0u;
+  }
+};
+
+constexpr float kMagic = 0x1.8p23f;
+
+// Eight codes: element i is x(i) divided by d(i).
+template <class GetX, class GetD>
+__device__ __forceinline__ u32x2_t codes8(GetX x, GetD d) {
+  uint32_t t[8];
+  bool off = false;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const float v = fmaf(x(i), d(i).r, kMagic);
+    const float rest = fmaf(kMagic - v, d(i).s, x(i));
+    off |= fabsf(rest) >= d(i).half;
+    t[i] = bits_of(v);
+  }
+  if (off) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float v = float_of(t[i]), rest = fmaf(kMagic - v, d(i).s, x(i));
+      const bool wrong = fabsf(rest) > d(i).half || (fabsf(rest) == d(i).half && (t[i] & 1));
+      if (wrong) t[i] = bits_of(v + (rest > 0.0f ? 1.0f : -1.0f));
+    }
+  }
+  u32x2_t c;
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const uint32_t lo = __builtin_amdgcn_perm(t[4 * h + 1], t[4 * h], 0x0C0C0400u);
+    const uint32_t hi = __builtin_amdgcn_perm(t[4 * h + 3], t[4 * h + 2], 0x0C0C0400u);
+    c[h] = lo | (hi << 16);
+  }
+  return c;
+}
+
+template <class T>
+__device__ __forceinline__ uint32_t largest(const Vec8<T> &v, uint32_t m) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) m = max(m, bits_of(v.at(i)) & 0x7FFFFFFFu);
+  return m;
+}
+
+// ---- rows alone -------------------------------------------------------------------------------
+
+// WAVES of a row; four rows a workgroup where that is one.  V vectors of eight a lane.
+template <class T, int WAVES, int V>
+__global__ void __launch_bounds__(WAVES == 1 ? 256 : WAVES * 64) rows_kernel(const RowQuantArgs a) {
+  constexpr int THREADS = WAVES * 64;
+  __shared__ uint32_t slot[WAVES];
+  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+  const int64_t row = WAVES == 1 ? (int64_t)blockIdx.x * 4 + wave : blockIdx.x;
+  if (WAVES == 1 && row >= a.rows) return;
+  const int at = (WAVES == 1 ? lane : (int)threadIdx.x) * 8;
+  const T *const x = (const T *)a.x + row * a.stride;
+  Vec8<T> v[V];
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    const int64_t e = at + i * THREADS * 8;
+    load8(v[i], x + e, a.cols - e);
+  }
+  uint32_t m = 0;
+#pragma unroll
+  for (int i = 0; i < V; ++i) m = largest(v[i], m);
+  m = row16_max(m);
+  m = max(m, (uint32_t)__shfl_xor((int)m, 16, 64));
+  m = max(m, (uint32_t)__shfl_xor((int)m, 32, 64));
+  if constexpr (WAVES > 1) {
+    if (lane == 0) slot[wave] = m;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < WAVES; ++w) m = max(m, slot[w]);
+  }
+  const Divide d(scale_of(m));
+  if (at == 0) a.scales[row] = d.s;
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    const int64_t e = at + i * THREADS * 8;
+    if (e >= a.pitch) break;
+    const u32x2_t c = codes8([&](int j) { return v[i].at(j); }, [&](int) { return d; });
+    *(u32x2_t *)(a.codes + row * a.pitch + e) = u32x2_t{c[0] & d.keep, c[1] & d.keep};
+  }
+}
+
+// ---- maxima over parts, then tiles --------------------------------------------------------------
+
+constexpr int kMostHigh = 4096;   // rows of a part: their maxima stay in LDS
+
+template <class T, bool ROWS, bool COLS>
+__global__ void __launch_bounds__(256) parts_kernel(const RowQuantArgs a) {
+  __shared__ uint32_t rmax[ROWS ? kMostHigh : 1];
+  __shared__ uint32_t cmax[4][128];
+  const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63, cg = tid & 15, rg = tid >> 4;
+  const int32_t pc = blockIdx.x % (uint32_t)a.parts_r, pr = blockIdx.x / (uint32_t)a.parts_r;
+  const int64_t r0 = (int64_t)pr * a.high;
+  const int high = (int)(a.rows - r0 < a.high ? a.rows - r0 : a.high);
+  if constexpr (ROWS) {
+    for (int i = tid; i < high; i += 256) rmax[i] = 0;
+    __syncthreads();
+  }
+  const int64_t b0 = (int64_t)pc * a.wide;
+  const int blocks = (int)(a.col_tiles - b0 < a.wide ? a.col_tiles - b0 : a.wide);
+  for (int b = 0; b < blocks; ++b) {
+    const int64_t c0 = (b0 + b) * 128 + cg * 8, nc = a.cols - c0;
+    uint32_t kmax[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) kmax[j] = 0;
+    constexpr int AHEAD = 8;   // rows of a lane whose loads are in flight together
+    for (int i0 = rg; i0 < high; i0 += 16 * AHEAD) {
+      Vec8<T> v[AHEAD];
+#pragma unroll
+      for (int u = 0; u < AHEAD; ++u) {
+        const int i = i0 + 16 * u;
+        load8(v[u], (const T *)a.x + (r0 + i) * a.stride + c0, i < high ? nc : 0);
+      }
+#pragma unroll
+      for (int u = 0; u < AHEAD; ++u) {
+        if constexpr (COLS) {
+#pragma unroll
+          for (int j = 0; j < 8; ++j) kmax[j] = max(kmax[j], bits_of(v[u].at(j)) & 0x7FFFFFFFu);
+        }
+        if constexpr (ROWS) {
+          const uint32_t m = row16_max(largest(v[u], 0));
+          if (cg == 0 && i0 + 16 * u < high) atomicMax(&rmax[i0 + 16 * u], m);
+        }
+      }
+    }
+    if constexpr (COLS) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        kmax[j] = max(kmax[j], (uint32_t)__shfl_xor((int)kmax[j], 16, 64));
+        kmax[j] = max(kmax[j], (uint32_t)__shfl_xor((int)kmax[j], 32, 64));
+      }
+      __syncthreads();   // the block before has been read
+      if (lane < 16) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) cmax[wave][cg * 8 + j] = kmax[j];
+      }
+      __syncthreads();
+      const int64_t c = (b0 + b) * 128 + tid;
+      if (tid < 128 && c < a.cols)
+        a.col_parts[pr * a.cols + c] =
+            max(max(cmax[0][tid], cmax[1][tid]), max(cmax[2][tid], cmax[3][tid]));
+    }
+  }
+  if constexpr (ROWS) {
+    __syncthreads();
+    for (int i = tid; i < high; i += 256) a.row_parts[pc * a.rows + r0 + i] = rmax[i];
+  }
+}
+
+// The bytes of the first n of eight codes; what lies past the matrix is stored as zeros.
+__device__ __forceinline__ u32x2_t first_bytes(u32x2_t c, int64_t n) {
+  if (n >= 8) return c;
+  const uint64_t keep = n <= 0 ? 0 : ~0ull >> (64 - 8 * n);
+  return u32x2_t{c[0] & (uint32_t)keep, c[1] & (uint32_t)(keep >> 32)};
+}
+
+// The scale of element i of `count` from its `parts` maxima.
+__device__ __forceinline__ float scale_of_parts(const uint32_t *p, int parts, int64_t count,
+                                                int64_t i) {
+  uint32_t m = 0;
+  for (int k = 0; k < parts; k += 8) {
+    uint32_t u[8];   // loads in flight together
+#pragma unroll
+    for (int j = 0; j < 8; ++j) u[j] = k + j < parts ? p[(k + j) * count + i] : 0;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) m = max(m, u[j]);
+  }
+  return scale_of(m);
+}
+
+template <class T, bool ROWS, bool COLS>
+__global__ void __launch_bounds__(256) tiles_kernel(const RowQuantArgs a) {
+  __shared__ float sr[128], sc[128];
+  __shared__ __align__(16) uint8_t turned[COLS ? 128 * 128 : 16];
+  const int tid = threadIdx.x, cg = tid & 15, rg = tid >> 4;
+  const int64_t ct = blockIdx.x % (uint32_t)a.col_tiles, rt = blockIdx.x / (uint32_t)a.col_tiles;
+  const int64_t c0 = ct * 128 + cg * 8, r0 = rt * 128 + rg * 8;
+  const int64_t nc = a.cols - c0, nr = a.rows - r0;
+  Vec8<T> v[8];
+#pragma unroll
+  for (int p = 0; p < 8; ++p)
+    load8(v[p], (const T *)a.x + (r0 + p) * a.stride + c0, p < nr ? nc : 0);
+  if (tid < 128) {
+    const int64_t r = rt * 128 + tid;
+    if (ROWS && r < a.rows) {
+      const float s = scale_of_parts(a.row_parts, a.parts_r, a.rows, r);
+      sr[tid] = s;
+      if (ct == 0) a.scales[r] = s;
+    }
+  } else {
+    const int64_t c = ct * 128 + tid - 128;
+    if (COLS && c < a.cols) {
+      const float s = scale_of_parts(a.col_parts, a.parts_c, a.cols, c);
+      sc[tid - 128] = s;
+      if (rt == 0) a.scales_t[c] = s;
+    }
+  }
+  __syncthreads();
+  if constexpr (ROWS) {
+#pragma unroll
+    for (int p = 0; p < 8; ++p) {
+      const Divide d(p < nr ? sr[rg * 8 + p] : 1.0f);
+      u32x2_t c = codes8([&](int i) { return v[p].at(i); }, [&](int) { return d; });
+      c = first_bytes(u32x2_t{c[0] & d.keep, c[1] & d.keep}, nc);
+      if (p < nr && c0 < a.pitch) *(u32x2_t *)(a.codes + (r0 + p) * a.pitch + c0) = c;
+    }
+  }
+  if constexpr (COLS) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const int col = cg * 8 + j;
+      const Divide d(j < nc ? sc[col] : 1.0f);
+      u32x2_t c = codes8([&](int i) { return v[i].at(j); }, [&](int) { return d; });
+      c = first_bytes(u32x2_t{c[0] & d.keep, c[1] & d.keep}, nr);
+      *(u32x2_t *)&turned[col * 128 + (((rg >> 1) ^ (cg & 7)) << 4) + (rg & 1) * 8] = c;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int col = i * 32 + (tid >> 3), chunk = tid & 7;
+      const u32x4_t w = *(const u32x4_t *)&turned[col * 128 + ((chunk ^ ((col >> 3) & 7)) << 4)];
+      const int64_t row_t = ct * 128 + col, at = rt * 128 + chunk * 16;
+      if (row_t < a.cols && at < a.pitch_t) *(u32x4_t *)(a.codes_t + row_t * a.pitch_t + at) = w;
+    }
+  }
+}
+
+// ---- choice -----------------------------------------------------------------------------------
+
+constexpr int64_t kMostInRow = 65536;   // columns that sixteen waves hold, eight vectors a lane
+
+template <class T>
+void launch_rows(const RowQuantArgs &a, hipStream_t s) {
+  const dim3 grid((uint32_t)a.rows), four((uint32_t)((a.rows + 3) / 4));
+  const int64_t n = a.cols;
+#define DG_ROWS(grid, waves, v) \
+  hipLaunchKernelGGL((rows_kernel<T, waves, v>), grid, dim3(waves == 1 ? 256 : waves * 64), 0, s, a)
+  if (n <= 512)
+    DG_ROWS(four, 1, 1);
+  else if (n <= 1024)
+    DG_ROWS(four, 1, 2);
+  else if (n <= 2048)
+    DG_ROWS(grid, 4, 1);
+  else if (n <= 4096)
+    DG_ROWS(grid, 4, 2);
+  else if (n <= 8192)
+    DG_ROWS(grid, 4, 4);
+  else if (n <= 16384)
+    DG_ROWS(grid, 16, 2);
+  else if (n <= 32768)
+    DG_ROWS(grid, 16, 4);
+  else
+    DG_ROWS(grid, 16, 8);
+#undef DG_ROWS
+}
+
+template <class T, bool ROWS, bool COLS>
+void launch_parts(const RowQuantArgs &a, hipStream_t s) {
+  const uint32_t parts = (uint32_t)a.parts_r * (uint32_t)a.parts_c;
+  const uint32_t tiles = (uint32_t)((a.rows + 127) / 128) * (uint32_t)a.col_tiles;
+  hipLaunchKernelGGL((parts_kernel<T, ROWS, COLS>), dim3(parts), dim3(256), 0, s, a);
+  hipLaunchKernelGGL((tiles_kernel<T, ROWS, COLS>), dim3(tiles), dim3(256), 0, s, a);
+}
+template <class T>
+void launch(const RowQuantArgs &a, hipStream_t s) {
+  if (!a.codes_t && a.cols <= kMostInRow)
+    launch_rows<T>(a, s);
+  else if (!a.codes_t)
+    launch_parts<T, true, false>(a, s);
+  else if (a.codes)
+    launch_parts<T, true, true>(a, s);
+  else
+    launch_parts<T, false, true>(a, s);
+}
+
+struct Parts {
+  int32_t parts_r, parts_c, wide, high;   // parts_r: of a row, so along the columns
+  size_t row_bytes, col_bytes;
+};
+Parts parts_of(int64_t rows, int64_t cols, bool rows_side, bool cols_side) {
+  Parts p{};
+  if (!cols_side && cols <= kMostInRow) return p;
+  const int64_t ct = (cols + 127) / 128;
+  p.wide = (int32_t)((ct + 15) / 16);
+  p.parts_r = (int32_t)((ct + p.wide - 1) / p.wide);
+  int64_t parts_c = std::min<int64_t>({64, 512 / p.parts_r, (rows + 31) / 32});
+  parts_c = std::max(parts_c, (rows + kMostHigh - 1) / kMostHigh);
+  p.high = (int32_t)((rows + parts_c - 1) / parts_c);
+  p.parts_c = (int32_t)((rows + p.high - 1) / p.high);
+  if (rows_side) p.row_bytes = (size_t)p.parts_r * (size_t)rows * 4;
+  if (cols_side) p.col_bytes = (size_t)p.parts_c * (size_t)cols * 4;
+  return p;
+}
+
+int check(int64_t rows, int64_t cols, bool rows_side, bool cols_side) {
+  if (rows < 0 || cols < 0 || (!rows_side && !cols_side)) return GEMM_ERR_INVALID_ARG;
+  if (rows == 0 || cols == 0) return GEMM_OK;
+  // 2^32 work-items, in tiles and in rows
+  if ((rows + 127) / 128 > 0xFFFFFF / ((cols + 127) / 128)) return GEMM_ERR_UNSUPPORTED;
+  if (!cols_side && rows > 0xFFFFFF / 4) return GEMM_ERR_UNSUPPORTED;
+  return GEMM_OK;
+}
+
+bool aligned(const void *p, uintptr_t n) { return ((uintptr_t)p & (n - 1)) == 0; }
+
+}  // namespace
+}  // namespace dg
+
+extern "C" int gemm_int8_quantize_workspace(int64_t rows, int64_t cols, int rows_side,
+                                            int cols_side, size_t *bytes) {
+  using namespace dg;
+  if (!bytes) return GEMM_ERR_INVALID_ARG;
+  const int st = check(rows, cols, rows_side != 0, cols_side != 0);
+  if (st != GEMM_OK) return st;
+  *bytes = 0;
+  if (rows == 0 || cols == 0) return GEMM_OK;
+  const Parts p = parts_of(rows, cols, rows_side != 0, cols_side != 0);
+  *bytes = p.row_bytes + p.col_bytes;
+  return GEMM_OK;
+}
+
+extern "C" int gemm_int8_quantize(const void *x, int dtype, int64_t rows, int64_t cols,
+                                  int64_t stride, void *codes, int64_t pitch, float *scales,
+                                  void *codes_t, int64_t pitch_t, float *scales_t, void *workspace,
+                                  size_t workspace_bytes, void *stream) {
+  using namespace dg;
+  if (dtype != GEMM_BF16 && dtype != GEMM_F32) return GEMM_ERR_INVALID_ARG;
+  const int st = check(rows, cols, codes != nullptr, codes_t != nullptr);
+  if (st != GEMM_OK) return st;
+  if (rows == 0 || cols == 0) return GEMM_OK;
+  if (!x || (codes && !scales) || (codes_t && !scales_t)) return GEMM_ERR_INVALID_ARG;
+  if (stride < 0 || (rows > 1 && stride < cols && stride != 0)) return GEMM_ERR_INVALID_ARG;
+  if (codes && (pitch < cols || pitch % 16 || pitch >= cols + 16)) return GEMM_ERR_INVALID_ARG;
+  if (codes_t && (pitch_t < rows || pitch_t % 16 || pitch_t >= rows + 16))
+    return GEMM_ERR_INVALID_ARG;
+  const Parts p = parts_of(rows, cols, codes != nullptr, codes_t != nullptr);
+  const size_t need = p.row_bytes + p.col_bytes;
+  if (need && (!workspace || workspace_bytes < need)) return GEMM_ERR_WORKSPACE;
+  if (!aligned(x, dtype == GEMM_BF16 ? 2 : 4) || !aligned(codes, 16) || !aligned(codes_t, 16) ||
+      !aligned(scales, 4) || !aligned(scales_t, 4) || !aligned(workspace, 4))
+    return GEMM_ERR_ALIGNMENT;
+  RowQuantArgs a{};
+  a.x = x;
+  a.rows = rows;
+  a.cols = cols;
+  a.stride = stride;
+  a.codes = (uint8_t *)codes;
+  a.codes_t = (uint8_t *)codes_t;
+  a.scales = scales;
+  a.scales_t = scales_t;
+  a.pitch = pitch;
+  a.pitch_t = pitch_t;
+  a.row_parts = (uint32_t *)workspace;
+  a.col_parts = (uint32_t *)((char *)workspace + p.row_bytes);
+  a.parts_r = p.parts_r;
+  a.parts_c = p.parts_c;
+  a.wide = p.wide;
+  a.high = p.high;
+  a.col_tiles = (int32_t)((cols + 127) / 128);
+  if (dtype == GEMM_BF16)
+    launch<bf16_t>(a, (hipStream_t)stream);
+  else
+    launch<float>(a, (hipStream_t)stream);
+  return hipGetLastError() == hipSuccess ? GEMM_OK : GEMM_ERR_HIP;
+}

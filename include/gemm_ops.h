@@ -3,10 +3,13 @@
  *
  *   gemm_block_quantize       e4m3 codes with one fp32 scale per block of 128
  *   gemm_block_run            C = A B^T of two such operands, with a bias or a source matrix
+ *   gemm_int8_quantize        int8 codes with one fp32 scale a row, and
+ *   gemm_int8_run             the product of two such operands
  *   gemm_layer_norm           layer norm, and
  *   gemm_layer_norm_backward  its gradients
  *   gemm_grad_norm            the norm of a list of gradients, and
  *   gemm_clip_grad_norm       the list scaled to a largest norm
+ *   gemm_adamw_step           an AdamW step over a list of parameters
  *
  * Conventions are those of gemm.h: every function returns a gemm_status, checks its arguments
  * before anything is enqueued, and enqueues kernels (nothing else) on `stream`; pointers are
@@ -110,6 +113,74 @@ int gemm_grad_norm(const gemm_tensor *list, int64_t count, float *norm, void *wo
  * GEMM_ERR_INVALID_ARG. */
 int gemm_clip_grad_norm(const gemm_tensor *list, int64_t count, float max_norm, float *norm,
                         void *workspace, size_t workspace_bytes, void *stream);
+
+/* int8 quantisation of the rows of x, rows x cols (GEMM_BF16 or GEMM_F32; element (i, j) at
+ * i * stride + j):
+ *   s = max(amax / 127, 2^-120) of each row, code = x / s, the exact quotient rounded to even, between
+ *   -127 and 127; NaN and zeros for a row that holds an infinity or a NaN.
+ * codes: rows x pitch bytes, pitch = cols rounded up to 16, zeros behind each row's codes; scales: one a
+ * row.  codes_t, scales_t: the same of x transposed (cols x rows).  Either side may be NULL.  codes and
+ * codes_t are 16-byte aligned. */
+int gemm_int8_quantize_workspace(int64_t rows, int64_t cols, int rows_side, int cols_side,
+                                 size_t *bytes);
+int gemm_int8_quantize(const void *x, int dtype, int64_t rows, int64_t cols, int64_t stride,
+                       void *codes, int64_t pitch, float *scales, void *codes_t, int64_t pitch_t,
+                       float *scales_t, void *workspace, size_t workspace_bytes, void *stream);
+
+/* A product of int8 operands with a scale a row of each: C (M x N, packed rows) =
+ *   scale_a[m] scale_b[n] * (sum over k of a b) + bias[n] + source[m, n].
+ * The sum is exact; it is rounded to fp32, and so is what follows, C once more to its type.  An element
+ * does not depend on the other rows and columns.  Scales are numbers of any size, or NaN; no step leaves
+ * fp32's range where the scaled sum is in it.  N at most 2^22, lda and ldb 2^22. */
+typedef struct {
+  int64_t M, N, K;
+  int64_t lda, ldb;            /* bytes from row to row: >= K, multiples of 16, zeros behind K  */
+  int32_t dtype_c;             /* GEMM_BF16 or GEMM_F32                                         */
+  int32_t dtype_source;        /* GEMM_BF16 or GEMM_F32; read where source is given             */
+} gemm_int8_desc;
+
+int gemm_int8_workspace(const gemm_int8_desc *desc, size_t *bytes);
+
+/* A, B 16-byte aligned; bias (N floats) and source (M x N, packed rows) or NULL.  The source may be C itself
+ * if it has C's type; where it, the bias or a scale overlaps C otherwise: GEMM_ERR_INVALID_ARG. */
+int gemm_int8_run(const gemm_int8_desc *desc, const void *A, const float *scale_a, const void *B,
+                  const float *scale_b, void *C, const float *bias, const void *source,
+                  void *workspace, size_t workspace_bytes, void *stream);
+
+/* One parameter of an AdamW step: numel packed elements of dtype (GEMM_BF16 or GEMM_F32), its gradient
+ * (dtype_grad), and where a bf16 copy of the stepped parameter goes, or NULL.  The list is host memory and
+ * is not needed after the call. */
+typedef struct {
+  void *param;
+  const void *grad;
+  void *copy;
+  int64_t numel;
+  int32_t dtype, dtype_grad;
+} gemm_adamw_tensor;
+
+/* The states of all parameters lie one after the other, each parameter's from a multiple of 128 elements
+ * on: GEMM_F32, or GEMM_FP8_E4M3 with a scale per 128 (m_scales, v_scales), where v holds the codes of its
+ * root.  (What lies between a parameter's last element and the next multiple of 128 counts as zero.) */
+typedef struct {
+  void *m, *v;                 /* fp32 4-byte, e4m3 8-byte aligned                              */
+  float *m_scales, *v_scales;
+  const float *norm;           /* of all gradients, which are scaled by
+                                  min(1, max_norm / (norm + 1e-6)); NULL: as they are           */
+  const float *lr_at;          /* where lr is in device memory, or NULL                         */
+  const int64_t *step_at;      /* where step is in device memory, or NULL                       */
+  int64_t step;                /* this step's number, from 1                                    */
+  double lr, beta1, beta2, eps, weight_decay, max_norm;
+  int32_t dtype_state;
+} gemm_adamw_desc;
+
+/* m = beta1 m + (1 - beta1) g, v = beta2 v + (1 - beta2) g^2, and
+ * param -= lr (weight_decay param + (m / (1 - beta1^step)) / (sqrt(v / (1 - beta2^step)) + eps)),
+ * in fp32, rounded once.  e4m3 states are rounded to nearest behind that: codes of x / s with
+ * s = max(amax / 448, 2^-126) of each 128 (NaN where they hold an infinity or a NaN), a root that is not
+ * zero never to zero.  Where something that is written overlaps anything else (a parameter that is in the
+ * list twice): GEMM_ERR_INVALID_ARG. */
+int gemm_adamw_step(const gemm_adamw_tensor *list, int64_t count, const gemm_adamw_desc *desc,
+                    void *stream);
 
 #ifdef __cplusplus
 }

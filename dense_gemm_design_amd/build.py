@@ -18,7 +18,8 @@ LIB = os.path.join(HERE, "libdgemm.so")
 SOURCES = [os.path.join(CSRC, name)
            for name in ("gemm.hip", "gemm_src_bf16.hip", "gemm_src_fp8.hip", "ops_block.hip",
                         "ops_block_wide.hip", "ops_quantize.hip", "ops_norm.hip", "ops_clip.hip",
-                        "ops_int8.hip", "ops_int8_quantize.hip", "ops_adamw.hip")]
+                        "ops_int8.hip", "ops_int8_wide.hip",
+                        "ops_int8_quantize.hip", "ops_adamw.hip")]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 

@@ -8,8 +8,12 @@
 #include "../../include/gemm_ops.h"
 #include "ops_int8.h"
 
+#include <initializer_list>
+
 namespace dg {
 namespace {
+
+constexpr int kCUs = 256;
 
 typedef i32x4 __attribute__((aligned(4))) i32x4_any;
 
@@ -19,27 +23,25 @@ __device__ __forceinline__ f32x4 floats(const i32x4 &v) {
 
 // ---- few rows ---------------------------------------------------------------------------------
 
-// Up to 16 FM rows of A: what counts is to read B once at the memory's rate.  A workgroup takes 16 GN
-// rows of B (columns of C); its eight waves take every eighth k-block (of its piece of K) straight
-// into registers, and their sums meet in LDS.
-template <int FM, int GN>
+// Up to 16 FM rows of A: what counts is to read B once at the memory's rate.  A workgroup takes 16 rows
+// of B (columns of C); its eight waves take every eighth k-block (of its piece of K) straight into
+// registers, and their sums meet in LDS.  1 x 4096 x 4096 takes 5.9 us (7.4 with 32 columns a workgroup), 1 x
+// 16384 x 16384 54 us, 5.0 TB/s.
+template <int FM>
 __global__ void __launch_bounds__(512) few_kernel(const Int8Args a) {
-  constexpr int WAVES = 8;
-  constexpr int AHEAD = FM * GN > 2 ? 2 : 4;   // k-blocks of a wave whose loads are in flight together
-  __shared__ int part[WAVES][FM][GN][16][17];
+  constexpr int WAVES = 8, AHEAD = 4;   // AHEAD: k-blocks of a wave whose loads are in flight together
+  __shared__ int part[WAVES][FM][16][17];
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
   const int r16 = lane & 15, g4 = lane >> 4;
-  const int64_t n0 = (int64_t)blockIdx.x * (16 * GN);
+  const int64_t n0 = (int64_t)blockIdx.x * 16;
   const auto ra = make_rsrc(a.A, a.M * a.lda);
-  const int64_t rows_b = a.N - n0 < 16 * GN ? a.N - n0 : 16 * GN;
+  const int64_t rows_b = a.N - n0 < 16 ? a.N - n0 : 16;
   const auto rb = make_rsrc(a.B + n0 * a.ldb, rows_b * a.ldb);
   const int split = blockIdx.y;
   const int32_t kb1 = (int32_t)((int64_t)a.kb * (split + 1) / a.splits);
-  i32x4 acc[FM][GN];
+  i32x4 acc[FM];
 #pragma unroll
-  for (int f = 0; f < FM; ++f)
-#pragma unroll
-    for (int g = 0; g < GN; ++g) acc[f][g] = i32x4{0, 0, 0, 0};
+  for (int f = 0; f < FM; ++f) acc[f] = i32x4{0, 0, 0, 0};
   // past K an operand reads as zeros
   auto take = [&](i32x4 (&q)[2], auto r, uint32_t row, uint32_t ld, uint32_t k) {
 #pragma unroll
@@ -50,14 +52,13 @@ __global__ void __launch_bounds__(512) few_kernel(const Int8Args a) {
   };
   for (int32_t kb0 = (int32_t)((int64_t)a.kb * split / a.splits) + wave; kb0 < kb1;
        kb0 += WAVES * AHEAD) {
-    i32x4 b[AHEAD][GN][2], x[AHEAD][FM][2];
+    i32x4 b[AHEAD][2], x[AHEAD][FM][2];
 #pragma unroll
     for (int u = 0; u < AHEAD; ++u) {
       const int32_t kb = kb0 + WAVES * u;
       // past the last k-block too
       const uint32_t k = kb < kb1 ? (uint32_t)kb * 128 + g4 * 32 : (uint32_t)a.kbytes;
-#pragma unroll
-      for (int g = 0; g < GN; ++g) take(b[u][g], rb, g * 16 + r16, (uint32_t)a.ldb, k);
+      take(b[u], rb, r16, (uint32_t)a.ldb, k);
 #pragma unroll
       for (int f = 0; f < FM; ++f) take(x[u][f], ra, f * 16 + r16, (uint32_t)a.lda, k);
     }
@@ -66,27 +67,22 @@ __global__ void __launch_bounds__(512) few_kernel(const Int8Args a) {
 #pragma unroll
       for (int h = 0; h < 2; ++h)
 #pragma unroll
-        for (int f = 0; f < FM; ++f)
-#pragma unroll
-          for (int g = 0; g < GN; ++g)
-            acc[f][g] = mfma_int8(b[u][g][h], x[u][f][h], acc[f][g]);
+        for (int f = 0; f < FM; ++f) acc[f] = mfma_int8(b[u][h], x[u][f][h], acc[f]);
   }
 #pragma unroll
   for (int f = 0; f < FM; ++f)
 #pragma unroll
-    for (int g = 0; g < GN; ++g)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) part[wave][f][g][r16][g4 * 4 + e] = acc[f][g][e];
+    for (int e = 0; e < 4; ++e) part[wave][f][r16][g4 * 4 + e] = acc[f][e];
   __syncthreads();
-  for (int i = threadIdx.x; i < FM * GN * 64; i += WAVES * 64) {
-    const int f = i / (64 * GN), g = i / 64 % GN, m16 = i / 4 % 16, q = i % 4;
-    const int64_t m = f * 16 + m16, n = n0 + g * 16 + q * 4;
+  for (int i = threadIdx.x; i < FM * 64; i += WAVES * 64) {
+    const int f = i / 64, m16 = i / 4 % 16, q = i % 4;
+    const int64_t m = f * 16 + m16, n = n0 + q * 4;
     if (m >= a.M || n >= a.N) continue;
     i32x4 v = {0, 0, 0, 0};
 #pragma unroll
     for (int w = 0; w < WAVES; ++w)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) v[e] += part[w][f][g][m16][q * 4 + e];
+      for (int e = 0; e < 4; ++e) v[e] += part[w][f][m16][q * 4 + e];
     if (a.splits == 1) {
       finish_four(a, m, n, floats(v));
       continue;
@@ -146,7 +142,7 @@ __device__ __forceinline__ void tile_corner(const Int8Args &a, int32_t t, int bm
   const int32_t strip = t / (8 * a.nt), in = t % (8 * a.nt);
   const int32_t high = a.mt - strip * 8 < 8 ? a.mt - strip * 8 : 8;
   m0 = (int64_t)(strip * 8 + in % high) * bm;
-  n0 = (int64_t)(in / high) * bn;
+  n0 = a.n_first + (int64_t)(in / high) * bn;
 }
 // The place of workgroup i of n, so that those of one XCD (i mod 8) are neighbours.
 __device__ __forceinline__ int32_t place(int32_t i, int32_t n) {
@@ -154,26 +150,89 @@ __device__ __forceinline__ int32_t place(int32_t i, int32_t n) {
   return x * per + (x < more ? x : more) + i / 8;
 }
 
+// Writes a lane's FM x FN quads of sums, quad (f, g) at row ml0 + 16 f and column nl0 + 16 g of the tile at
+// (m0, n0): as they are to its piece of the partial sums, or finished to C.
+template <int BM, int BN, int FM, int FN, class Get>
+__device__ __forceinline__ void write_blocks(const Int8Args &a, int32_t piece, int64_t m0, int64_t n0,
+                                             int ml0, int nl0, Get get) {
+  if (piece >= 0 || a.N < 4) {
+#pragma unroll
+    for (int f = 0; f < FM; ++f) {
+      const int ml = ml0 + f * 16;
+#pragma unroll
+      for (int g = 0; g < FN; ++g) {
+        const int nl = nl0 + g * 16;
+        const i32x4 v = get(f, g);
+        if (m0 + ml >= a.M || n0 + nl >= a.N) continue;
+        if (piece >= 0)
+          *(i32x4 *)((int *)a.partials + (int64_t)piece * (BM * BN) + ml * BN + nl) = v;
+        else
+          finish_four(a, m0 + ml, n0 + nl, floats(v));
+      }
+    }
+    return;
+  }
+  f32x4 bias[FN], sb[FN];
+#pragma unroll
+  for (int g = 0; g < FN; ++g) {
+    bias[g] = bias_four(a, n0 + nl0 + g * 16);
+    sb[g] = vector_four(a, a.sb, n0 + nl0 + g * 16);
+  }
+  float sa[FM];
+#pragma unroll
+  for (int f = 0; f < FM; ++f) {
+    const int64_t m = m0 + ml0 + f * 16;
+    sa[f] = a.sa[m < a.M ? m : a.M - 1];
+  }
+  with_source(a, [&](auto src_c) {
+    constexpr int SRC = decltype(src_c)::value, STEP = FM < 2 ? 1 : 2;
+#pragma unroll
+    for (int f0 = 0; f0 < FM; f0 += STEP) {
+      u32x4 src[STEP][FN];
+      if constexpr (SRC != SRC_NONE) {
+#pragma unroll
+        for (int f = 0; f < STEP; ++f)
+#pragma unroll
+          for (int g = 0; g < FN; ++g)
+            src[f][g] = source_at<SRC>(a, m0 + ml0 + (f0 + f) * 16, n0 + nl0 + g * 16);
+      }
+#pragma unroll
+      for (int f = 0; f < STEP; ++f)
+#pragma unroll
+        for (int g = 0; g < FN; ++g) {
+          const int64_t m = m0 + ml0 + (f0 + f) * 16, n = n0 + nl0 + g * 16;
+          f32x4 v = floats(get(f0 + f, g));
+          if (m >= a.M || n >= a.N) continue;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) v[e] = scaled(v[e], sa[f0 + f], sb[g][e], bias[g][e]);
+          if constexpr (SRC != SRC_NONE) v += source_four<SRC>(a, n, src[f][g]);
+          put_four(a, m, n, v);
+        }
+    }
+  });
+}
+
 // KG groups of WGM x WGN waves own a BM x BN tile of C, each for every KG-th k-block; their sums meet
-// in LDS.  Each group has a ring of S stages in LDS: the k-block that is multiplied, and S - 1 that are on
-// their way (loads that write LDS directly, rows swizzled in 16-byte chunks).  One barrier a step: behind
-// it every wave's loads of this step have landed, and its reads of the step before are done, whose
-// stage the next loads go to.
+// in LDS.  A ring of S stages in LDS holds the KG k-blocks that are multiplied, and S - KG that are on their
+// way (loads that write LDS directly, by all waves, rows swizzled in 16-byte chunks).  One barrier a step:
+// behind it every wave's loads of this step's blocks have landed, and its reads of the step before are done,
+// whose stages the next loads go to.
 //
 // The first a.whole tiles have a workgroup each; the k-blocks of the others are cut into a.splits
 // pieces, whose sums join_tiles_kernel adds.
 template <int BM, int BN, int WGM, int WGN, int KG, int S>
 __global__ void __launch_bounds__(KG *WGM *WGN * 64) tile_kernel(const Int8Args a) {
   constexpr int NW = WGM * WGN, WM = BM / WGM, WN = BN / WGN, FM = WM / 16, FN = WN / 16;
-  constexpr int LA = BM / 8 / NW, LB = BN / 8 / NW;   // 1 KiB loads (8 rows) a wave and stage
-  constexpr int STAGE = (BM + BN) * 128;
-  static_assert(LA * 8 * NW == BM && LB * 8 * NW == BN, "whole loads");
-  static_assert((S - 2) * (LA + LB) <= 63, "vmcnt");
-  static_assert(KG * S * STAGE <= 160 * 1024, "LDS");
-  __shared__ __align__(1024) char smem_[KG * S * STAGE];
+  constexpr int ALL = KG * NW;                           // waves
+  constexpr int LA = BM / 8 / ALL, LB = BN / 8 / ALL;    // 1 KiB loads (8 rows) a wave and stage
+  constexpr int STAGE = (BM + BN) * 128, AHEAD = S - KG;
+  static_assert(LA * 8 * ALL == BM && LB * 8 * ALL == BN, "whole loads");
+  static_assert(AHEAD >= KG && (AHEAD - KG) * (LA + LB) <= 63, "vmcnt");
+  static_assert(S * STAGE <= 160 * 1024, "LDS");
+  __shared__ __align__(1024) char smem_[S * STAGE];
+  lds_t *const smem = (lds_t *)smem_;
   const int wave_ = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
   const int group = wave_ / NW, wave = wave_ % NW;
-  lds_t *const smem = (lds_t *)smem_ + group * S * STAGE;
 
   const int32_t i = blockIdx.x, cut = a.mt * a.nt - a.whole;   // tiles whose K is cut
   int32_t t, piece = -1, kb0 = 0, kb1 = a.kb;   // piece: of the partial sums
@@ -196,28 +255,31 @@ __global__ void __launch_bounds__(KG *WGM *WGN * 64) tile_kernel(const Int8Args 
   const int32_t rows_b = (int32_t)(a.N - n0 < BN ? a.N - n0 : BN);
   const auto ra = make_rsrc(a.A + m0 * a.lda, (int64_t)rows_a * a.lda);
   const auto rb = make_rsrc(a.B + n0 * a.ldb, (int64_t)rows_b * a.ldb);
-  const uint32_t row0 = wave * 8 + lane / 8;
+  const uint32_t row0 = wave_ * 8 + lane / 8;
   const uint32_t chunk = ((lane % 8) ^ ((row0 >> 1) & 7)) * 16;
   const uint32_t voa = row0 * (uint32_t)a.lda + chunk, vob = row0 * (uint32_t)a.ldb + chunk;
   const uint32_t kend =
       (uint32_t)(kb1 * 128 < a.kbytes ? kb1 * 128 : a.kbytes);   // a piece ends inside K
-  // (a step past the end loads zeros: as many loads are in flight in every step)
-  auto load_stage = [&](int32_t kb, int s) {
-    const uint32_t k = (uint32_t)kb * 128;
-    const bool past = k + chunk >= kend;
-    lds_t *const to = smem + s * STAGE + wave * 1024;
+  uint32_t kload = (uint32_t)kb0 * 128;   // of the next block to load
+  int sload = 0;                          // and its stage
+  // (a block past the end loads zeros: as many loads are in flight in every step)
+  auto load_next = [&] {
+    const bool past = kload + chunk >= kend;
+    lds_t *const to = smem + sload * STAGE + wave_ * 1024;
     // rows past the edge lie past the range of the buffer: their lanes read zeros
-    const uint32_t oa = past ? kOOB : voa + k, ob = past ? kOOB : vob + k;
+    const uint32_t oa = past ? kOOB : voa + kload, ob = past ? kOOB : vob + kload;
 #pragma unroll
     for (int j = 0; j < LA; ++j)
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(ra, to + j * NW * 1024, 16,
-                                               oa + (uint32_t)(j * NW * 8) * (uint32_t)a.lda, 0, 0,
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(ra, to + j * ALL * 1024, 16,
+                                               oa + (uint32_t)(j * ALL * 8) * (uint32_t)a.lda, 0, 0,
                                                0);
 #pragma unroll
     for (int j = 0; j < LB; ++j)
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(rb, to + BM * 128 + j * NW * 1024, 16,
-                                               ob + (uint32_t)(j * NW * 8) * (uint32_t)a.ldb, 0, 0,
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rb, to + BM * 128 + j * ALL * 1024, 16,
+                                               ob + (uint32_t)(j * ALL * 8) * (uint32_t)a.ldb, 0, 0,
                                                0);
+    kload += 128;
+    sload = sload == S - 1 ? 0 : sload + 1;
   };
 
   // consumer
@@ -238,14 +300,15 @@ __global__ void __launch_bounds__(KG *WGM *WGN * 64) tile_kernel(const Int8Args 
   const bool inside = m0 + wm * WM < a.M && n0 + wn * WN < a.N;
 
 #pragma unroll
-  for (int s = 0; s < S - 1; ++s) load_stage(kb0 + group + s * KG, s);
-  int s = 0;
+  for (int j = 0; j < AHEAD; ++j) load_next();
+  int s = group;
   for (int32_t kb = kb0 + group; kb < kb1 + group; kb += KG) {   // as often in every group
-    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"((S - 2) * (LA + LB))
+    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"((AHEAD - KG) * (LA + LB))
                  : "memory");
-    load_stage(kb + (S - 1) * KG, s == 0 ? S - 1 : s - 1);
+#pragma unroll
+    for (int j = 0; j < KG; ++j) load_next();
     const lds_t *const st = smem + s * STAGE;
-    s = s == S - 1 ? 0 : s + 1;
+    s = s + KG >= S ? s + KG - S : s + KG;
     if (!inside || kb >= kb1) continue;
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
@@ -264,16 +327,16 @@ __global__ void __launch_bounds__(KG *WGM *WGN * 64) tile_kernel(const Int8Args 
   asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
 
   // each group gives away the sums of the rows of blocks that the other one writes
-  constexpr int OWN = FM / KG;
-  static_assert(KG == 1 || (KG == 2 && OWN * KG == FM && NW * OWN * FN * 1024 <= S * STAGE), "");
+  constexpr int OWN = FM / KG, HALF = NW * OWN * FN * 1024;
+  static_assert(KG == 1 || (KG == 2 && OWN * KG == FM && 2 * HALF <= S * STAGE), "");
   if constexpr (KG == 2) {
     typedef i32x4 __attribute__((address_space(3))) *i4p;
-    lds_t *const area = (lds_t *)smem_ + wave * (OWN * FN * 1024) + lane * 16;
+    lds_t *const area = smem + wave * (OWN * FN * 1024) + lane * 16;
 #pragma unroll
     for (int f = 0; f < OWN; ++f)
 #pragma unroll
       for (int g = 0; g < FN; ++g)
-        *(i4p)(area + (group ^ 1) * S * STAGE + (f * FN + g) * 1024) =
+        *(i4p)(area + (group ^ 1) * HALF + (f * FN + g) * 1024) =
             group ? acc[f][g] : acc[f + OWN][g];
     asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
 #pragma unroll
@@ -281,126 +344,333 @@ __global__ void __launch_bounds__(KG *WGM *WGN * 64) tile_kernel(const Int8Args 
 #pragma unroll
       for (int g = 0; g < FN; ++g)
         acc[f][g] = (group ? acc[f + OWN][g] : acc[f][g]) +
-                    *(i4p)(area + group * S * STAGE + (f * FN + g) * 1024);
+                    *(i4p)(area + group * HALF + (f * FN + g) * 1024);
   }
   const int ml0 = wm * WM + group * OWN * 16 + r16, nl0 = wn * WN + g4 * 4;
-  if (piece >= 0 || a.N < 4) {
-#pragma unroll
-    for (int f = 0; f < OWN; ++f) {
-      const int ml = ml0 + f * 16;
-      if (m0 + ml >= a.M) continue;
-#pragma unroll
-      for (int g = 0; g < FN; ++g) {
-        const int nl = nl0 + g * 16;
-        if (n0 + nl >= a.N) continue;
-        if (piece >= 0)
-          *(i32x4 *)((int *)a.partials + (int64_t)piece * (BM * BN) + ml * BN + nl) = acc[f][g];
-        else
-          finish_four(a, m0 + ml, n0 + nl, floats(acc[f][g]));
-      }
+  write_blocks<BM, BN, OWN, FN>(a, piece, m0, n0, ml0, nl0,
+                                [&](int f, int g) { return acc[f][g]; });
+}
+
+// Tiles of BM x BN, four waves of half of their rows and columns, each alone on its SIMD, the instruction
+// stream laid out by hand as in the wide kernel (ops_int8_wide.hip): in each slot behind a block's two MFMAs
+// goes a share of what the next steps need.  A ring of S stages in LDS: behind the handshake of step c the
+// next step's loads have landed and this step's fragments are all read, so that step c + S may be loaded to
+// their stage.  A workgroup stays for one item (a tile, or a piece of one's K)
+// after the other, and the loads run ahead into the next.
+struct Item {
+  int64_t m0, n0;
+  int32_t kb0, kb1, piece;
+};
+// Item `round` of worker b; false if there is none.
+__device__ __forceinline__ bool item_at(const Int8Args &a, int32_t b, int32_t round, int bm, int bn,
+                                        Item &w) {
+  const int32_t cut = a.mt * a.nt - a.whole, all = a.whole + cut * a.splits, first = round * kCUs;
+  if (first + b >= all) return false;
+  const int32_t i = first + place(b, all - first < kCUs ? all - first : kCUs);
+  int32_t t = i;
+  w.piece = -1;
+  w.kb0 = 0;
+  w.kb1 = a.kb;
+  if (i >= a.whole) {
+    const int32_t split = (i - a.whole) / cut, at = (i - a.whole) % cut;
+    t = a.whole + at;
+    w.piece = a.splits > 1 ? split * cut + at : -1;
+    w.kb0 = (int32_t)((int64_t)a.kb * split / a.splits);
+    w.kb1 = (int32_t)((int64_t)a.kb * (split + 1) / a.splits);
+  }
+  tile_corner(a, t, bm, bn, w.m0, w.n0);
+  return true;
+}
+
+template <int BM, int BN, int S>
+__global__ void __attribute__((amdgpu_flat_work_group_size(256, 256), amdgpu_waves_per_eu(1, 1)))
+pipe_kernel(const Int8Args a) {
+  constexpr int NW = 4, WM = BM / 2, WN = BN / 2, FM = WM / 16, FN = WN / 16, NM = FM * FN;
+  constexpr int LA = BM / 8 / NW, LB = BN / 8 / NW, L = LA + LB;
+  constexpr int STAGE = (BM + BN) * 128;
+  static_assert(S * STAGE <= 160 * 1024 && (S - 2) * L <= 63, "");
+  __shared__ __align__(1024) char smem_[S * STAGE];
+  lds_t *const smem = (lds_t *)smem_;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
+  const int wm = wave / 2, wn = wave % 2, r16 = lane & 15, g4 = lane >> 4;
+
+  // ---- producer: the k-block to load next, its stage, and where its item lies
+  int32_t pround = 0, pk = 0, pend = 0;
+  int pstage = 0;
+  __amdgpu_buffer_rsrc_t ra = uniform_rsrc(a.A, 0), rb = ra;
+  const uint32_t row0 = wave * 8 + lane / 8;
+  const uint32_t chunk = ((lane % 8) ^ ((row0 >> 1) & 7)) * 16;
+  const uint32_t stepa = NW * 8 * (uint32_t)a.lda, stepb = NW * 8 * (uint32_t)a.ldb;
+  const uint32_t oa = row0 * (uint32_t)a.lda + chunk, ob = row0 * (uint32_t)a.ldb + chunk;
+  auto producer_item = [&] {
+    Item w;
+    if (item_at(a, blockIdx.x, pround, BM, BN, w)) {
+      const int32_t rows_a = (int32_t)(a.M - w.m0 < BM ? a.M - w.m0 : BM);
+      const int32_t rows_b = (int32_t)(a.N - w.n0 < BN ? a.N - w.n0 : BN);
+      pk = w.kb0;
+      pend = w.kb1;
+      ra = uniform_rsrc(a.A + w.m0 * a.lda, rows_a * a.lda);
+      rb = uniform_rsrc(a.B + w.n0 * a.ldb, rows_b * a.ldb);
+    } else {   // empty ranges read as zeros
+      pk = 0;
+      pend = 1 << 30;
+      ra = uniform_rsrc(a.A, 0);
+      rb = ra;   // (in the order of the other branch, or both are kept in memory)
     }
-    return;
-  }
-  f32x4 bias[FN], sb[FN];
-#pragma unroll
-  for (int g = 0; g < FN; ++g) {
-    bias[g] = bias_four(a, n0 + nl0 + g * 16);
-    sb[g] = vector_four(a, a.sb, n0 + nl0 + g * 16);
-  }
-  float sa[OWN];
-#pragma unroll
-  for (int f = 0; f < OWN; ++f) {
-    const int64_t m = m0 + ml0 + f * 16;
-    sa[f] = a.sa[m < a.M ? m : a.M - 1];
-  }
-  with_source(a, [&](auto src_c) {
-    constexpr int SRC = decltype(src_c)::value, STEP = OWN < 2 ? 1 : 2;
-#pragma unroll
-    for (int f0 = 0; f0 < OWN; f0 += STEP) {
-      u32x4 src[STEP][FN];
-      if constexpr (SRC != SRC_NONE) {
-#pragma unroll
-        for (int f = 0; f < STEP; ++f)
-#pragma unroll
-          for (int g = 0; g < FN; ++g)
-            src[f][g] = source_at<SRC>(a, m0 + ml0 + (f0 + f) * 16, n0 + nl0 + g * 16);
-      }
-#pragma unroll
-      for (int f = 0; f < STEP; ++f)
-#pragma unroll
-        for (int g = 0; g < FN; ++g) {
-          const int64_t m = m0 + ml0 + (f0 + f) * 16, n = n0 + nl0 + g * 16;
-          if (m >= a.M || n >= a.N) continue;
-          f32x4 v = floats(acc[f0 + f][g]);
-#pragma unroll
-          for (int e = 0; e < 4; ++e) v[e] = scaled(v[e], sa[f0 + f], sb[g][e], bias[g][e]);
-          if constexpr (SRC != SRC_NONE) v += source_four<SRC>(a, n, src[f][g]);
-          put_four(a, m, n, v);
-        }
+  };
+  uint32_t la, lb;
+  lds_t *to;
+  auto begin = [&] {
+    const uint32_t k = (uint32_t)pk * 128;
+    const bool past = k + chunk >= (uint32_t)a.kbytes;
+    la = past ? kOOB : oa + k;
+    lb = past ? kOOB : ob + k;
+    to = smem + pstage * STAGE + wave * 1024;
+  };
+  // load J of the k-block: eight rows of A or of B.  A row past the tile's edge lies past its
+  // buffer's range and reads as zeros.
+  auto load = [&](auto j_c) {
+    constexpr int J = decltype(j_c)::value;
+    if constexpr (J < LA)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(ra, to + J * NW * 1024, 16, la + J * stepa, 0, 0, 0);
+    else
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rb, to + BM * 128 + (J - LA) * NW * 1024, 16,
+                                               lb + (J - LA) * stepb, 0, 0, 0);
+  };
+  auto end = [&] {
+    pstage = pstage == S - 1 ? 0 : pstage + 1;
+    if (++pk == pend) {
+      ++pround;
+      producer_item();
     }
-  });
+  };
+
+  // ---- consumer
+  const uint32_t x = (r16 >> 1) & 7;
+  const uint32_t ck[2] = {(g4 ^ x) * 16, ((g4 + 4) ^ x) * 16};
+  const uint32_t arow = (wm * WM + r16) * 128, brow = BM * 128 + (wn * WN + r16) * 128;
+  typedef const i32x4 __attribute__((address_space(3))) *frag;
+  i32x4 fa[2][FM], fb[2][FN], acc[FM][FN];
+  // fragment E of a half: B's first
+  auto read = [&](const lds_t *st, auto half_c, auto e_c) {
+    constexpr int H = decltype(half_c)::value, E = decltype(e_c)::value;
+    if constexpr (E < FN)
+      fb[H][E] = *(frag)(st + brow + ck[H] + E * 2048);
+    else
+      fa[H][E - FN] = *(frag)(st + arow + ck[H] + (E - FN) * 2048);
+  };
+  producer_item();
+#pragma unroll
+  for (int s = 0; s < S; ++s) {
+    begin();
+    [&]<int... J>(std::integer_sequence<int, J...>) {
+      (load(std::integral_constant<int, J>()), ...);
+    }(std::make_integer_sequence<int, L>());
+    end();
+  }
+  asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" ::"n"((S - 1) * L < 63 ? (S - 1) * L : 63) : "memory");
+  [&]<int... E>(std::integer_sequence<int, E...>) {
+    (read(smem, std::integral_constant<int, 0>(), std::integral_constant<int, E>()), ...);
+  }(std::make_integer_sequence<int, FM + FN>());
+
+  int stage = 0;   // of the step
+  auto kstep = [&](auto first_c) {
+    const lds_t *const now = smem + stage * STAGE;
+    stage = stage == S - 1 ? 0 : stage + 1;
+    const lds_t *const next = smem + stage * STAGE;
+    // what was moved or made ready between steps is two wait states old before an MFMA reads it
+    asm volatile("s_nop 1" ::: "memory");
+    int8_step<FM, FN, L>(
+        [&](auto half_c, auto f_c, auto g_c) {
+          constexpr int H = decltype(half_c)::value, f = decltype(f_c)::value, g = decltype(g_c)::value;
+          if constexpr (decltype(first_c)::value && H == 0)
+            mfma_int8_zero(acc[f][g], fb[H][g], fa[H][f]);
+          else
+            mfma_int8_inplace(acc[f][g], fb[H][g], fa[H][f]);
+        },
+        [&](auto half_c, auto e_c) { read(decltype(half_c)::value ? now : next, half_c, e_c); },
+        [&] {
+          asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"((S - 2) * L) : "memory");
+          begin();
+        },
+        load);
+    end();
+  };
+  Item w;
+  for (int32_t round = 0; item_at(a, blockIdx.x, round, BM, BN, w); ++round) {
+    kstep(std::true_type());
+    for (int32_t kb = w.kb0 + 1; kb < w.kb1; ++kb) kstep(std::false_type());
+    mfma_wait_states();
+    write_blocks<BM, BN, FM, FN>(a, w.piece, w.m0, w.n0, wm * WM + r16, wn * WN + g4 * 4,
+                                 [&](int f, int g) {
+                                   return i32x4{acc_read(acc[f][g][0]), acc_read(acc[f][g][1]),
+                                                acc_read(acc[f][g][2]), acc_read(acc[f][g][3])};
+                                 });
+  }
+  wait_vmcnt<0>();   // no load is on its way into LDS that the workgroup no longer has
 }
 
 // Adds the pieces of the tiles whose K is cut, then the epilogue.  1024 elements of a tile a workgroup.
-template <int BM, int BN>
 __global__ void __launch_bounds__(256) join_tiles_kernel(const Int8Args a) {
-  constexpr int QUADS = BN / 4, GROUPS = BM * BN / 1024;
-  const int32_t cut = a.mt * a.nt - a.whole, at = blockIdx.x / GROUPS;
-  const int i = blockIdx.x % GROUPS * 256 + threadIdx.x;
-  const int ml = i / QUADS, nl = i % QUADS * 4;
+  const int32_t size = a.bm * a.bn, quads = a.bn / 4, groups = size / 1024;
+  const int32_t cut = a.mt * a.nt - a.whole, at = blockIdx.x / groups;
+  const int32_t i = blockIdx.x % groups * 256 + threadIdx.x;
+  const int32_t ml = i / quads, nl = i % quads * 4;
   int64_t m0, n0;
-  tile_corner(a, a.whole + at, BM, BN, m0, n0);
+  tile_corner(a, a.whole + at, a.bm, a.bn, m0, n0);
   const int64_t m = m0 + ml, n = n0 + nl;
   if (m >= a.M || n >= a.N) return;
   finish_four(a, m, n,
-              joined((const int *)a.partials + (int64_t)at * (BM * BN) + ml * BN + nl,
-                     (int64_t)cut * (BM * BN), a.splits, 4));
+              joined((const int *)a.partials + (int64_t)at * size + ml * a.bn + nl, (int64_t)cut * size,
+                     a.splits, 4));
 }
 
 // ---- choice -----------------------------------------------------------------------------------
 
-constexpr int kCUs = 256;
-
-enum { PLAN_FEW, PLAN_128 };
-struct Int8Plan {
-  int kind, splits;
-  int32_t bm, bn, mt, nt, whole;   // whole: the tiles whose K is not cut
+// Kernels for tiles, and what a launch of one takes by measurement (us): each of a workgroup's items `fix`
+// and, for each k-block, `alone` where few CUs are at work to `full` where all are, which then share the way
+// to the caches and the power.  (At 4096 x 4096, rows against us by each kernel, smallest tile to largest:
+// 64: 10.2, 14.1, 17.1; 256: 11.5, 14.4, 18.0; 512: 20, 15.7, 18.3; 1024: 36, 27, 22.0, 24.8, 30.4, 28.6, 47;
+// 2048: 71, 55, 40, 46, 36, 34.8, 47.)
+struct TileKind {
+  int32_t bm, bn;
+  double fix, alone, full;
+  void (*launch)(const Int8Args &, hipStream_t);
 };
-
-Int8Plan plan_of(const gemm_int8_desc &d) {
-  const int64_t kb = (d.K + 127) / 128;
-  const int64_t least = kb > kMostBlocks ? (kb + kMostBlocks - 1) / kMostBlocks : 1;   // of pieces
-  if (d.M <= 64) {
-    const int cols = 16;
-    const int64_t nt = (d.N + cols - 1) / cols;
-    int64_t splits = nt < 128 ? 256 / nt : 1;
-    if (splits > kb / 16) splits = kb / 16;
-    if (splits < least) splits = least;
-    return {PLAN_FEW, splits > 1 ? (int)splits : 1, 0, 0, 1, (int32_t)nt, 0};
-  }
-  const int64_t mt = (d.M + 127) / 128, nt = (d.N + 127) / 128, t = mt * nt;
-  int64_t splits = least;
-  if (t < kCUs / 2 && kb >= 16) splits = kCUs / t;
-  if (splits > kb / 8) splits = kb / 8;
-  if (splits < least) splits = least;
-  return {PLAN_128, (int)splits, 128, 128, (int32_t)mt, (int32_t)nt,
-          (int32_t)(splits > 1 ? 0 : t)};
-}
-
-template <int FM, int GN>
-void launch_few(const Int8Args &a, hipStream_t s) {
-  const dim3 grid((uint32_t)a.nt, (uint32_t)a.splits);
-  hipLaunchKernelGGL((few_kernel<FM, GN>), grid, dim3(512), 0, s, a);
-}
 template <int BM, int BN, int WGM, int WGN, int KG, int S>
 void launch_tiles(const Int8Args &a, hipStream_t s) {
   const dim3 grid((uint32_t)(a.whole + (a.mt * a.nt - a.whole) * a.splits));
   hipLaunchKernelGGL((tile_kernel<BM, BN, WGM, WGN, KG, S>), grid, dim3(KG * WGM * WGN * 64), 0, s,
                      a);
-  if (a.splits > 1)
-    hipLaunchKernelGGL((join_tiles_kernel<BM, BN>),
-                       dim3((uint32_t)((a.mt * a.nt - a.whole) * (BM * BN / 1024))), dim3(256), 0,
-                       s, a);
+}
+template <int BM, int BN, int S>
+void launch_pipe(const Int8Args &a, hipStream_t s) {
+  const int64_t items = a.whole + (int64_t)(a.mt * a.nt - a.whole) * a.splits;
+  hipLaunchKernelGGL((pipe_kernel<BM, BN, S>), dim3((uint32_t)(items < kCUs ? items : kCUs)), dim3(256), 0,
+                     s, a);
+}
+constexpr TileKind kTiles[] = {
+    {64, 64, 1.2, 0.185, 0.245, launch_tiles<64, 64, 2, 2, 2, 8>},
+    {64, 128, 2.0, 0.32, 0.36, launch_pipe<64, 128, 5>},
+    {128, 128, 3.2, 0.385, 0.51, launch_pipe<128, 128, 4>},
+    {128, 192, 3.8, 0.52, 0.64, launch_pipe<128, 192, 4>},
+    {192, 128, 3.8, 0.52, 0.64, launch_pipe<192, 128, 4>},
+    {192, 192, 4.5, 0.70, 0.93, launch_pipe<192, 192, 3>},
+    {128, 256, 4.6, 0.64, 0.88, launch_pipe<128, 256, 3>},
+    {256, 128, 4.6, 0.64, 0.88, launch_pipe<256, 128, 3>},
+};
+constexpr int kWide = 256;                       // of the wide kernel's tiles
+constexpr double kWideAlone = 1.0, kWideFull = 1.38;
+// Its rounds write beside the next one's first step; an fp32 C, and rows that are no multiple of four columns,
+// are written before it.  (4096 x 4096 x 4096 bf16 54.5 us, fp32 64.)
+double wide_fix(const gemm_int8_desc &d) {
+  return d.dtype_c == GEMM_BF16 && d.N % 4 == 0 ? 5.0 : 15.0;
+}
+constexpr double kWideLast = 2.5, kBehind = 4.0;   // us behind the last round; of a second launch
+constexpr double kLaunch = 2.2, kBytes = 5.0e6;  // us of a launch; bytes a us from memory
+
+struct Int8Plan {
+  int tiles;               // of kTiles; -1: few rows; -2: none, all columns are the wide kernel's
+  int32_t wide;            // columns of the wide kernel's tiles in front
+  int32_t splits, mt, nt, whole;   // whole: the tiles whose K is not cut
+};
+
+double rounds_of(double items, double blocks, double fix, double alone, double full) {
+  const double rounds = (double)((int64_t)items / kCUs), rest = items - rounds * kCUs;
+  double us = rounds * (fix + blocks * full);
+  if (rest > 0) us += fix + blocks * (alone + (full - alone) * rest / kCUs);
+  return us;
+}
+
+// The best of kTiles for N columns, and its time.
+double best_tiles(const gemm_int8_desc &d, int64_t N, int64_t kb, int64_t least, Int8Plan &best) {
+  double us = 1e30;
+  for (int k = 0; k < (int)(sizeof(kTiles) / sizeof(kTiles[0])); ++k) {
+    const TileKind &t = kTiles[k];
+    const int64_t mt = (d.M + t.bm - 1) / t.bm, nt = (N + t.bn - 1) / t.bn, all = mt * nt;
+    const auto offer = [&](double time, int64_t splits, int64_t whole) {
+      if (time >= us) return;
+      us = time;
+      best.tiles = k;
+      best.splits = (int32_t)splits;
+      best.mt = (int32_t)mt;
+      best.nt = (int32_t)nt;
+      best.whole = (int32_t)whole;
+    };
+    if (least == 1) offer(kLaunch + rounds_of((double)all, (double)kb, t.fix, t.alone, t.full), 1, all);
+    // K cut for the tiles that do not fill a round: a launch, and 8 bytes an element and piece
+    const int64_t whole = least == 1 ? all / kCUs * kCUs : 0, rest = all - whole;
+    if (rest == 0 || (least == 1 && rest > kCUs / 2)) continue;
+    for (int64_t s : {2, 3, 4, 6, 8, 12, 16, 24, 32, 48, 64}) {
+      if (s < least && least > 64) s = least;
+      if (s < least || (s > least && (s * 4 > kb || rest * s > 2 * kCUs))) continue;
+      const double items = (double)(rest * s), blocks = (double)((kb + s - 1) / s);
+      offer(kLaunch + rounds_of((double)whole, (double)kb, t.fix, t.alone, t.full) +
+                rounds_of(items, blocks, t.fix, t.alone, t.full) + 3.6 +
+                items * (double)(t.bm * t.bn) * 2.8e-6,
+            s, whole);
+      if (least > 64) break;
+    }
+  }
+  return us;
+}
+
+Int8Plan plan_of(const gemm_int8_desc &d) {
+  const int64_t kb = (d.K + 127) / 128;
+  const int64_t least = kb > kMostBlocks ? (kb + kMostBlocks - 1) / kMostBlocks : 1;   // of pieces
+  Int8Plan best{};
+  double us = best_tiles(d, d.N, kb, least, best);
+  const double memory = (double)(d.M + d.N) * (double)d.K / kBytes;
+  if (us < kLaunch + memory) us = kLaunch + memory;
+  if (d.M <= 32) {
+    // Few rows: 16 columns a workgroup, that reads them and all rows of A at 34 bytes a ns, all together
+    // at 7600; K in pieces where there are few columns and much of it.  (us so, and on tiles: 1 x 4096 x 4096
+    // 5.9, 9.4; 16 x 4096 x 4096 6.9, 9.6; 1 x 14336 x 4096 13.0, 11.8; 16 x 16384 x 16384 76, 62.)
+    const int64_t nt = (d.N + 15) / 16;
+    const double group = (double)(16 + d.M) * (double)d.K;
+    for (int64_t s = least; s <= 64; s = s * 2) {
+      if (s > least && (nt * s > kCUs || s * 8 > kb)) break;
+      double t = group / 34e3 / (double)s;
+      const double way = (double)nt * group / 7.6e6;
+      t = t < way ? way : t;
+      t = 2.4 + (t < memory ? memory : t);
+      if (s > 1) t += 2.4 + (double)(s * d.M * d.N) * 2.8e-6;
+      if (t < us || (best.tiles >= 0 && least > 64)) {
+        us = t;
+        best = {-1, 0, (int32_t)s, 1, (int32_t)nt, 0};
+      }
+    }
+    return best;
+  }
+  if (d.N < 4 || kb == 0 || least > 1) return best;
+  // Tiles of 256 x 256, all columns or as many of them as fill rounds of all CUs, the others' tiles in a launch
+  // behind them.  (4096 x 14336 x 4096, 3.5 rounds: all 184 us, three rounds and 256 tiles of 128 x 256 192;
+  // 4096 x 4352 x 4096, 272 tiles: 89, one round and others 66.)
+  const int64_t mt = (d.M + kWide - 1) / kWide, nt = (d.N + kWide - 1) / kWide;
+  const double fix = wide_fix(d);
+  const double all =
+      kLaunch + kWideLast + rounds_of((double)(mt * nt), (double)kb, fix, kWideAlone, kWideFull);
+  if (all < us) {
+    us = all;
+    best = {-2, (int32_t)nt, 1, 0, 0, 0};
+  }
+  const int64_t front = mt * nt / kCUs * kCUs / mt;   // columns of tiles
+  if (front > 0 && front < nt) {
+    Int8Plan rest{};
+    const double t =
+        kBehind + kWideLast + rounds_of((double)(mt * front), (double)kb, fix, kWideAlone, kWideFull) +
+        best_tiles(d, d.N - front * kWide, kb, 1, rest);
+    if (t < us) {
+      best = rest;
+      best.wide = (int32_t)front;
+    }
+  }
+  return best;
+}
+
+template <int FM>
+void launch_few(const Int8Args &a, hipStream_t s) {
+  hipLaunchKernelGGL(few_kernel<FM>, dim3((uint32_t)a.nt, (uint32_t)a.splits), dim3(512), 0, s, a);
 }
 
 int check(const gemm_int8_desc *d) {
@@ -412,15 +682,16 @@ int check(const gemm_int8_desc *d) {
   // offsets inside a tile of 256 rows (of A, B or C) stay under 31 bits, work-items under 2^32
   if (d->lda > (1 << 22) || d->ldb > (1 << 22)) return GEMM_ERR_UNSUPPORTED;
   if (d->M > (1ll << 31) || d->N > (1ll << 22)) return GEMM_ERR_UNSUPPORTED;
-  if (((d->M + 127) / 128) * ((d->N + 127) / 128) > (1ll << 22)) return GEMM_ERR_UNSUPPORTED;
+  if (((d->M + 63) / 64) * ((d->N + 63) / 64) > (1ll << 22)) return GEMM_ERR_UNSUPPORTED;
   return GEMM_OK;
 }
 
 size_t workspace_of(const gemm_int8_desc &d, const Int8Plan &p) {
   if (p.splits <= 1) return 0;
-  return (size_t)p.splits * sizeof(int) *
-         (p.kind == PLAN_FEW ? (size_t)d.M * (size_t)d.N
-                             : (size_t)(p.mt * p.nt - p.whole) * (size_t)(p.bm * p.bn));
+  const size_t one = p.tiles < 0 ? (size_t)d.M * (size_t)d.N
+                                 : (size_t)(p.mt * p.nt - p.whole) *
+                                       (size_t)(kTiles[p.tiles].bm * kTiles[p.tiles].bn);
+  return (size_t)p.splits * sizeof(int) * one;
 }
 
 }  // namespace
@@ -480,28 +751,42 @@ extern "C" int gemm_int8_run(const gemm_int8_desc *d, const void *A, const float
   a.ldb = d->ldb;
   a.kbytes = (int32_t)((d->K + 15) / 16 * 16);
   a.kb = (int32_t)((d->K + 127) / 128);
+  a.out_bf16 = d->dtype_c == GEMM_BF16;
+  a.src_bf16 = d->dtype_source == GEMM_BF16;
+  a.plain_rows = !source && a.out_bf16 && d->N % 4 == 0 && !((uintptr_t)C & 7);
+  hipStream_t s = (hipStream_t)stream;
+  if (p.wide > 0) {
+    a.mt = (int32_t)((d->M + kWide - 1) / kWide);
+    a.nt = p.wide;
+    if (launch_int8_wide(a, s) != hipSuccess) return GEMM_ERR_HIP;
+    if (p.tiles == -2) return GEMM_OK;
+  }
+  a.n_first = (int64_t)p.wide * kWide;
   a.mt = p.mt;
   a.nt = p.nt;
   a.splits = p.splits;
   a.whole = p.whole;
-  a.out_bf16 = d->dtype_c == GEMM_BF16;
-  a.src_bf16 = d->dtype_source == GEMM_BF16;
-  a.plain_rows = !source && (d->N * (a.out_bf16 ? 2 : 4)) % 16 == 0 && !((uintptr_t)C & 15);
-  hipStream_t s = (hipStream_t)stream;
-  if (p.kind == PLAN_FEW) {
+  if (p.tiles < 0) {
     if (d->M <= 16)
-      launch_few<1, 1>(a, s);
-    else if (d->M <= 32)
-      launch_few<2, 1>(a, s);
+      launch_few<1>(a, s);
     else
-      launch_few<4, 1>(a, s);
-    if (p.splits > 1) {
-      const int64_t need_wg = (d->M * ((d->N + 3) / 4) + 255) / 256;
-      hipLaunchKernelGGL(join_kernel, dim3((uint32_t)(need_wg < 8 * kCUs ? need_wg : 8 * kCUs)),
-                         dim3(256), 0, s, a);
-    }
+      launch_few<2>(a, s);
   } else {
-    launch_tiles<128, 128, 2, 2, 2, 2>(a, s);
+    a.bm = kTiles[p.tiles].bm;
+    a.bn = kTiles[p.tiles].bn;
+    kTiles[p.tiles].launch(a, s);
   }
-  return hipGetLastError() == hipSuccess ? GEMM_OK : GEMM_ERR_HIP;
+  if (hipGetLastError() != hipSuccess) return GEMM_ERR_HIP;
+  if (p.splits > 1) {
+    const int64_t few = (d->M * ((d->N + 3) / 4) + 255) / 256;
+    if (p.tiles < 0)
+      hipLaunchKernelGGL(join_kernel, dim3((uint32_t)(few < 8 * kCUs ? few : 8 * kCUs)), dim3(256), 0, s,
+                         a);
+    else
+      hipLaunchKernelGGL(join_tiles_kernel,
+                         dim3((uint32_t)((p.mt * p.nt - p.whole) * (a.bm * a.bn / 1024))), dim3(256), 0, s,
+                         a);
+    if (hipGetLastError() != hipSuccess) return GEMM_ERR_HIP;
+  }
+  return GEMM_OK;
 }

@@ -612,15 +612,16 @@ PyObject *adamw_step(PyObject *, PyObject *const *arg, Py_ssize_t) {
     On on;
     std::vector<gemm_adamw_tensor> list((size_t)params.size());
     int64_t blocks = 0;
-    const auto here = [&](const std::string &name, const at::Tensor &t) {
-      if (!t.is_cuda() || (on.device >= 0 && t.get_device() != on.device)) on(name, t);
+    // (names are made only for what is refused: a list of 193 takes 4 us so)
+    const auto elsewhere = [&](const at::Tensor &t) {
+      if (!t.is_cuda() || (on.device >= 0 && t.get_device() != on.device)) return true;
       on.device = t.get_device();
+      return false;
     };
     for (Py_ssize_t i = 0; i < params.size(); ++i) {
       const auto name = [&](const char *kind) { return kind + (" " + std::to_string(i)); };
-      for (PyObject *o : {params[i], grads[i]})
-        if (!THPVariable_Check(o))
-          throw Refused(name(o == params[i] ? "parameter" : "gradient") + " must be a torch tensor");
+      if (!THPVariable_Check(params[i])) throw Refused(name("parameter") + " must be a torch tensor");
+      if (!THPVariable_Check(grads[i])) throw Refused(name("gradient") + " must be a torch tensor");
       const at::Tensor &p = THPVariable_Unpack(params[i]), &g = THPVariable_Unpack(grads[i]);
       if (!plain(p)) refuse_layout(name("parameter"), p);
       if (!plain(g)) refuse_layout(name("gradient"), g);
@@ -629,17 +630,17 @@ PyObject *adamw_step(PyObject *, PyObject *const *arg, Py_ssize_t) {
       if (!is_type(g.scalar_type()) || !g.is_contiguous() || g.sizes() != p.sizes())
         refuse(name("gradient"), g, "packed float32 or bfloat16 " + list_of(p.sizes()) +
                                         " like its parameter");
-      here(name("parameter"), p);
-      here(name("gradient"), g);
+      if (elsewhere(p)) on(name("parameter"), p);
+      if (elsewhere(g)) on(name("gradient"), g);
       gemm_adamw_tensor &t = list[(size_t)i];
       t = gemm_adamw_tensor{p.data_ptr(), g.data_ptr(), nullptr, p.numel(),
                             gemm_type(p.scalar_type()), gemm_type(g.scalar_type())};
       blocks += up(t.numel, 128);
       if (copying && copies[i] != Py_None) {
-        const at::Tensor &c = tensor(name("copy"), copies[i]);
+        const at::Tensor &c = tensor("copy", copies[i]);
         if (c.scalar_type() != at::kBFloat16 || !c.is_contiguous() || c.sizes() != p.sizes())
           refuse(name("copy"), c, "packed bfloat16 " + list_of(p.sizes()) + " like its parameter");
-        here(name("copy"), c);
+        if (elsewhere(c)) on(name("copy"), c);
         t.copy = c.data_ptr();
       }
     }
@@ -658,7 +659,7 @@ PyObject *adamw_step(PyObject *, PyObject *const *arg, Py_ssize_t) {
         refuse(names[k], t, std::string("a packed vector of ") + std::to_string(n) +
                                 (e4m3 && k < 2 ? ", float8_e4m3fn or uint8" : ", torch.float32") +
                                 ", as adamw_state gives");
-      here(names[k], t);
+      if (elsewhere(t)) on(names[k], t);
     }
     d.m = state[0].data_ptr();
     d.v = state[1].data_ptr();

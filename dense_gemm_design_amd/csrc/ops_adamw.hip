@@ -13,32 +13,44 @@
 // The list goes to the kernels as a table in their arguments, as in ops_clip.hip, cut into chunks that
 // workgroups take in turn.  A lane takes eight neighbours, so a scale's 128 are a DPP row of 16 lanes.
 //
-// Bound by memory: parameters and states read and written once, gradients read once.
+// Bound by memory: parameters and states read and written once, gradients read once.  Many short workgroups
+// come nearest to it (310 M bf16 parameters with e4m3 states, 2.6 GB, in chunks of 2048, 4096, 8192, 16384:
+// 511, 466, 469, 498 us, 5.65 TB/s at best; 160 M fp32 ones with fp32 states and copies, 3.8 GB, of 1024, 2048,
+// 4096, 16384: 640, 676, 733, 768 us, 5.9 TB/s; 2048 workgroups that stay: 556, 831), and loads and stores
+// past the caches (583 and 860 without).
 #include "../../include/gemm_ops.h"
 #include "ops_common.h"
 #include "ops_spans.h"
 
 #include <math.h>
 
+#include <type_traits>
+
 namespace dg {
 namespace {
 
-constexpr int kTable = 88;           // tensors a launch: the table stays under 4 KB of arguments
+constexpr int kTable = 120, kTableCopies = 96;   // tensors a launch: a table stays under 4 KB of arguments
 constexpr int kBlock = 128;          // neighbours of one scale; each tensor's state starts at a multiple
 constexpr int kThreads = 256;
-constexpr int kChunkLeast = kThreads * 8, kChunkMost = 16384;   // elements a workgroup takes at once
-constexpr int kGroups = 2048;        // workgroups a launch, at most
-constexpr int64_t kLongest = (int64_t)1 << 37;   // of all tensors: chunks fit 31 bits, blocks 32
+constexpr int kGroups = 1 << 22;     // workgroups a launch, at most: chunks past them are second ones
+constexpr int64_t kLongest = (int64_t)1 << 37;   // of all tensors: chunks and blocks fit 32 bits
+constexpr int64_t kPassing = 96 << 20;   // bytes of a step that the caches could keep for the next pass
 
-struct Table {
-  void *param[kTable];
-  const void *grad[kTable];
-  void *copy[kTable];
-  int64_t n[kTable];
-  uint32_t block[kTable];       // the first block of 128 of each tensor's state
-  uint32_t first[kTable + 1];   // first chunk of each tensor; first[count] = all of them
-  uint32_t f32[3];              // bit i: tensor i's parameters are fp32, else bf16
-  uint32_t grad_f32[3];
+template <int N>
+struct Copies {
+  void *copy[N];
+};
+struct NoCopies {};
+template <bool COPIES>
+struct Table : std::conditional_t<COPIES, Copies<kTableCopies>, NoCopies> {
+  static constexpr int N = COPIES ? kTableCopies : kTable;
+  void *param[N];
+  const void *grad[N];
+  int64_t n[N];
+  uint32_t block[N];            // the first block of 128 of each tensor's state
+  uint32_t first[N + 1];        // first chunk of each tensor; first[count] = all of them
+  uint32_t f32[4];              // bit i: tensor i's parameters are fp32, else bf16
+  uint32_t grad_f32[4];
   int32_t count, chunk;
 };
 struct Step {
@@ -50,19 +62,23 @@ struct Step {
   float b1, b1_rest, b2, b2_rest, eps, decay, max_norm;
   float lr, rate, root;         // rate = lr / (1 - b1^t), root = 1 / sqrt(1 - b2^t)
 };
-static_assert(sizeof(Table) + sizeof(Step) + 16 <= 4096, "kernel arguments");
-static_assert(kTable <= 96, "bits of the types");
+static_assert(sizeof(Table<false>) + sizeof(Step) + 16 <= 4096, "kernel arguments");
+static_assert(sizeof(Table<true>) + sizeof(Step) + 16 <= 4096, "kernel arguments");
+static_assert(kTable <= 128, "bits of the types, two tensors a lane");
 
-__device__ __forceinline__ int tensor_of(const Table &t, uint32_t chunk) {
-  int lo = 0, hi = t.count - 1;   // the last tensor whose first chunk is not past it
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if (t.first[mid] <= chunk)
-      lo = mid;
-    else
-      hi = mid - 1;
+// The last tensor whose first chunk is not past this one.  Arguments may lie in the host's memory: all first
+// chunks in one trip there, not the seven of a search that halves them.
+template <class T>
+__device__ __forceinline__ int tensor_of(const T &t, uint32_t chunk) {
+  const int lane = threadIdx.x & 63;
+  int n = 0;
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    const int i = lane + 64 * k;
+    const bool at = i < t.count && t.first[i < T::N ? i : 0] <= chunk;
+    n += __builtin_popcountll(__builtin_amdgcn_ballot_w64(at));
   }
-  return lo;
+  return __builtin_amdgcn_readfirstlane(n - 1);
 }
 
 __device__ __forceinline__ double power(double b, int64_t t) {
@@ -147,68 +163,130 @@ __device__ __forceinline__ void update(const Step &a, const Now &now, float g, f
   p = fmaf(-now.decay, p, p) - way;
 }
 
-// One vector of eight of a tensor: element e of it, of which `n` are left.
-template <class P, class G, bool E4M3>
+// W neighbours of a tensor as fp32, of which n are there; ONCE: past the caches, for lists too long for them.
+template <int W, bool ONCE, class T>
+__device__ __forceinline__ void take(float (&x)[W], const T *p, int64_t n) {
+  if (n >= W) {
+    if constexpr (W == 8) {
+      Vec8<T> v;
+      if constexpr (ONCE)
+        v.load_once(p);
+      else
+        v.load(p);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) x[i] = v.at(i);
+    } else if constexpr (sizeof(T) == 4) {
+      const u32x4_t v = ONCE ? __builtin_nontemporal_load((const u32x4_any *)p) : *(const u32x4_any *)p;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) x[i] = float_of(v[i]);
+    } else {
+      const u32x2_t v = ONCE ? __builtin_nontemporal_load((const u32x2_any *)p) : *(const u32x2_any *)p;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) x[i] = float_of(i & 1 ? v[i / 2] & 0xFFFF0000u : v[i / 2] << 16);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < W; ++i) x[i] = i < n ? load1(p + i) : 0.0f;
+  }
+}
+template <int W, bool ONCE, class T>
+__device__ __forceinline__ void give(T *p, const float (&x)[W], int64_t n) {
+  if (n >= W) {
+    if constexpr (W == 8) {
+      if constexpr (ONCE)
+        store8_once(p, x);
+      else
+        store8_full(p, x);
+    } else if constexpr (sizeof(T) == 4) {
+      const u32x4_t v = {bits_of(x[0]), bits_of(x[1]), bits_of(x[2]), bits_of(x[3])};
+      if constexpr (ONCE)
+        __builtin_nontemporal_store(v, (u32x4_any *)p);
+      else
+        *(u32x4_any *)p = v;
+    } else {
+      const u32x2_t v = {bf16_pair(x[0], x[1]), bf16_pair(x[2], x[3])};
+      if constexpr (ONCE)
+        __builtin_nontemporal_store(v, (u32x2_any *)p);
+      else
+        *(u32x2_any *)p = v;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < W; ++i)
+      if (i < n) store1(p + i, x[i]);
+  }
+}
+template <bool ONCE>
+__device__ __forceinline__ u32x2_t take_codes(const void *p, int64_t at) {
+  const u32x2_t *q = (const u32x2_t *)((const uint8_t *)p + at);
+  return ONCE ? __builtin_nontemporal_load(q) : *q;
+}
+template <bool ONCE>
+__device__ __forceinline__ void give_codes(void *p, int64_t at, u32x2_t c) {
+  u32x2_t *q = (u32x2_t *)((uint8_t *)p + at);
+  if (ONCE)
+    __builtin_nontemporal_store(c, q);
+  else
+    *q = c;
+}
+
+// Neighbours of a lane: eight of a block's 128 with e4m3 states; four with fp32 states, whose 16 bytes then
+// lie next to the next lane's.
+template <bool E4M3>
+constexpr int kWidth = E4M3 ? 8 : 4;
+
+// One vector of a tensor, of which `n` elements are left.
+template <class P, class G, bool E4M3, bool ONCE>
 __device__ __forceinline__ void vector_step(const Step &a, const Now &now, P *p, const G *g,
                                             bf16_t *copy, int64_t state, int64_t n) {
-  Vec8<P> pv;
-  Vec8<G> gv;
-  load8(pv, p, n);
-  load8(gv, g, n);
-  float m[8], v[8], x[8], r[8];
+  constexpr int W = kWidth<E4M3>;
+  float m[W], v[W], x[W], d[W], r[W];
+  take<W, ONCE>(x, p, n);
+  take<W, ONCE>(d, g, n);
   if constexpr (E4M3) {
     u32x2_t mc = {0, 0}, vc = {0, 0};
     float ms = 0.0f, vs = 0.0f;
     if (n > 0) {
-      mc = *(const u32x2_t *)((const uint8_t *)a.m + state);
-      vc = *(const u32x2_t *)((const uint8_t *)a.v + state);
+      mc = take_codes<ONCE>(a.m, state);
+      vc = take_codes<ONCE>(a.v, state);
       ms = a.ms[state / kBlock];
       vs = a.vs[state / kBlock];
     }
     decode8(m, mc, ms);
     decode8(v, vc, vs);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] *= v[i];
+    for (int i = 0; i < W; ++i) v[i] *= v[i];
   } else {
-    Vec8<float> mv, vv;
-    load8(mv, (const float *)a.m + state, n);
-    load8(vv, (const float *)a.v + state, n);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      m[i] = mv.at(i);
-      v[i] = vv.at(i);
-    }
+    take<W, ONCE>(m, (const float *)a.m + state, n);
+    take<W, ONCE>(v, (const float *)a.v + state, n);
   }
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    x[i] = pv.at(i);
-    update(a, now, gv.at(i), x[i], m[i], v[i], r[i]);
-  }
-  store8(p, x, n);
-  if (copy) store8(copy, x, n);
+  for (int i = 0; i < W; ++i) update(a, now, d[i], x[i], m[i], v[i], r[i]);
+  give<W, ONCE>(p, x, n);
+  if (copy) give<W, ONCE>(copy, x, n);
   if constexpr (E4M3) {
     // what lies behind the tensor's end is no part of its last block
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
+    for (int i = 0; i < W; ++i)
       if (i >= n) m[i] = r[i] = 0.0f;
     float ms, vs;
     const u32x2_t mc = encode8<false>(m, &ms), vc = encode8<true>(r, &vs);
     if (n > 0) {
-      *(u32x2_t *)((uint8_t *)a.m + state) = mc;
-      *(u32x2_t *)((uint8_t *)a.v + state) = vc;
+      give_codes<ONCE>(a.m, state, mc);
+      give_codes<ONCE>(a.v, state, vc);
       if (state % kBlock == 0) {
         a.ms[state / kBlock] = ms;
         a.vs[state / kBlock] = vs;
       }
     }
   } else {
-    store8((float *)a.m + state, m, n);
-    store8((float *)a.v + state, v, n);
+    give<W, ONCE>((float *)a.m + state, m, n);
+    give<W, ONCE>((float *)a.v + state, v, n);
   }
 }
 
-template <bool E4M3>
-__global__ void __launch_bounds__(kThreads) adamw_kernel(const Table t, const Step a) {
+template <bool E4M3, bool COPIES, bool ONCE>
+__global__ void __launch_bounds__(kThreads) adamw_kernel(const Table<COPIES> t, const Step a) {
   Now now{1.0f, a.rate, a.root, a.lr * a.decay};
   if (a.step_at || a.lr_at) {
     float lr = a.lr;
@@ -233,14 +311,18 @@ __global__ void __launch_bounds__(kThreads) adamw_kernel(const Table t, const St
     const int64_t at = (int64_t)(c - t.first[i]) * t.chunk;
     const int64_t n = t.n[i] - at < t.chunk ? t.n[i] - at : t.chunk;
     const int64_t state = (int64_t)t.block[i] * kBlock + at;
-    bf16_t *const copy = t.copy[i] ? (bf16_t *)t.copy[i] + at : nullptr;
+    bf16_t *copy = nullptr;
+    if constexpr (COPIES)
+      if (t.copy[i]) copy = (bf16_t *)t.copy[i] + at;
     auto run = [&](auto param, auto grad) {
       using P = decltype(param);
       using G = decltype(grad);
       P *const p = (P *)t.param[i] + at;
       const G *const g = (const G *)t.grad[i] + at;
-      for (int64_t e = threadIdx.x * 8; e - threadIdx.x * 8 < n; e += kThreads * 8)
-        vector_step<P, G, E4M3>(a, now, p + e, g + e, copy ? copy + e : nullptr, state + e, n - e);
+      constexpr int W = kWidth<E4M3>;
+      for (int64_t e = threadIdx.x * W; e - threadIdx.x * W < n; e += kThreads * W)
+        vector_step<P, G, E4M3, ONCE>(a, now, p + e, g + e, copy ? copy + e : nullptr, state + e,
+                                      n - e);
     };
     const bool pf = (t.f32[i / 32] >> (i % 32)) & 1, gf = (t.grad_f32[i / 32] >> (i % 32)) & 1;
     if (pf && gf)
@@ -319,6 +401,42 @@ int check_apart(const gemm_adamw_tensor *list, int64_t count, const gemm_adamw_d
   });
 }
 
+// Enqueues a launch for each table that the list fills; `all` elements are in it.
+template <bool E4M3, bool COPIES, bool ONCE>
+int step_list(const gemm_adamw_tensor *list, int64_t count, const Step &a, int64_t all,
+              hipStream_t s) {
+  Table<COPIES> t;
+  // a vector a thread; two with e4m3 states where that leaves every CU some workgroups
+  t.chunk = kThreads * kWidth<E4M3>;
+  if (E4M3 && all >= (int64_t)4096 * t.chunk) t.chunk *= 2;
+  int64_t i = 0, block = 0;
+  while (i < count) {
+    t.count = 0;
+    t.first[0] = 0;
+    for (int w = 0; w < 4; ++w) t.f32[w] = t.grad_f32[w] = 0;
+    for (; i < count && t.count < t.N; ++i) {
+      const gemm_adamw_tensor &x = list[i];
+      if (x.numel == 0) continue;
+      const int k = t.count++;
+      t.param[k] = x.param;
+      t.grad[k] = x.grad;
+      if constexpr (COPIES) t.copy[k] = x.copy;
+      t.n[k] = x.numel;
+      t.block[k] = (uint32_t)block;
+      if (x.dtype == GEMM_F32) t.f32[k / 32] |= 1u << (k % 32);
+      if (x.dtype_grad == GEMM_F32) t.grad_f32[k / 32] |= 1u << (k % 32);
+      t.first[k + 1] = t.first[k] + (uint32_t)((x.numel + t.chunk - 1) / t.chunk);
+      block += (x.numel + kBlock - 1) / kBlock;
+    }
+    if (t.count == 0) break;
+    const uint32_t chunks = t.first[t.count];
+    const dim3 grid(chunks < (uint32_t)kGroups ? chunks : kGroups);
+    hipLaunchKernelGGL((adamw_kernel<E4M3, COPIES, ONCE>), grid, dim3(kThreads), 0, s, t, a);
+    if (hipGetLastError() != hipSuccess) return GEMM_ERR_HIP;
+  }
+  return GEMM_OK;
+}
+
 }  // namespace
 }  // namespace dg
 
@@ -351,39 +469,26 @@ extern "C" int gemm_adamw_step(const gemm_adamw_tensor *list, int64_t count,
     a.rate = (float)((d->lr_at ? 1.0 : d->lr) / (1.0 - pow(d->beta1, (double)d->step)));
     a.root = (float)(1.0 / sqrt(1.0 - pow(d->beta2, (double)d->step)));
   }
-  int64_t all = 0;
-  for (int64_t i = 0; i < count; ++i) all += list[i].numel;
-  Table t;
-  t.chunk = kChunkMost;
-  while (t.chunk > kChunkLeast && all / t.chunk < kGroups) t.chunk /= 2;
-  int64_t i = 0, block = 0;
-  while (i < count) {
-    t.count = 0;
-    t.first[0] = 0;
-    for (int w = 0; w < 3; ++w) t.f32[w] = t.grad_f32[w] = 0;
-    for (; i < count && t.count < kTable; ++i) {
-      const gemm_adamw_tensor &x = list[i];
-      if (x.numel == 0) continue;
-      const int k = t.count++;
-      t.param[k] = x.param;
-      t.grad[k] = x.grad;
-      t.copy[k] = x.copy;
-      t.n[k] = x.numel;
-      t.block[k] = (uint32_t)block;
-      if (x.dtype == GEMM_F32) t.f32[k / 32] |= 1u << (k % 32);
-      if (x.dtype_grad == GEMM_F32) t.grad_f32[k / 32] |= 1u << (k % 32);
-      t.first[k + 1] = t.first[k] + (uint32_t)((x.numel + t.chunk - 1) / t.chunk);
-      block += (x.numel + kBlock - 1) / kBlock;
-    }
-    if (t.count == 0) break;
-    const uint32_t chunks = t.first[t.count];
-    const dim3 grid(chunks < (uint32_t)kGroups ? chunks : kGroups);
-    hipStream_t s = (hipStream_t)stream;
-    if (d->dtype_state == GEMM_F32)
-      hipLaunchKernelGGL((adamw_kernel<false>), grid, dim3(kThreads), 0, s, t, a);
-    else
-      hipLaunchKernelGGL((adamw_kernel<true>), grid, dim3(kThreads), 0, s, t, a);
-    if (hipGetLastError() != hipSuccess) return GEMM_ERR_HIP;
+  bool copies = false;
+  int64_t all = 0, bytes = 0;
+  for (int64_t i = 0; i < count; ++i) {
+    const gemm_adamw_tensor &x = list[i];
+    copies = copies || (x.numel && x.copy);
+    all += x.numel;
+    bytes += x.numel * ((x.dtype == GEMM_F32 ? 8 : 4) + (x.dtype_grad == GEMM_F32 ? 4 : 2) +
+                        (d->dtype_state == GEMM_F32 ? 16 : 4) + (x.copy ? 2 : 0));
   }
-  return GEMM_OK;
+  const bool once = bytes > kPassing, e4m3 = d->dtype_state == GEMM_FP8_E4M3;
+  hipStream_t s = (hipStream_t)stream;
+  const auto go = [&](auto e4m3_c, auto copies_c, auto once_c) {
+    return step_list<decltype(e4m3_c)::value, decltype(copies_c)::value, decltype(once_c)::value>(
+        list, count, a, all, s);
+  };
+  const auto with_once = [&](auto e4m3_c, auto copies_c) {
+    return once ? go(e4m3_c, copies_c, std::true_type()) : go(e4m3_c, copies_c, std::false_type());
+  };
+  const auto with_copies = [&](auto e4m3_c) {
+    return copies ? with_once(e4m3_c, std::true_type()) : with_once(e4m3_c, std::false_type());
+  };
+  return e4m3 ? with_copies(std::true_type()) : with_copies(std::false_type());
 }

@@ -560,13 +560,13 @@ constexpr TileKind kTiles[] = {
     {256, 128, 4.6, 0.64, 0.88, launch_pipe<256, 128, 3>},
 };
 constexpr int kWide = 256;                       // of the wide kernel's tiles
-constexpr double kWideAlone = 1.0, kWideFull = 1.38;
+constexpr double kWideAlone = 0.95, kWideFull = 1.37;
 // Its rounds write beside the next one's first step; an fp32 C, and rows that are no multiple of four columns,
 // are written before it.  (4096 x 4096 x 4096 bf16 54.5 us, fp32 64.)
 double wide_fix(const gemm_int8_desc &d) {
-  return d.dtype_c == GEMM_BF16 && d.N % 4 == 0 ? 5.0 : 15.0;
+  return d.dtype_c == GEMM_BF16 && d.N % 4 == 0 ? 3.7 : 13.0;
 }
-constexpr double kWideLast = 2.5, kBehind = 4.0;   // us behind the last round; of a second launch
+constexpr double kWideOnce = 6.0;   // us before the first round and behind the last
 constexpr double kLaunch = 2.2, kBytes = 5.0e6;  // us of a launch; bytes a us from memory
 
 struct Int8Plan {
@@ -643,22 +643,23 @@ Int8Plan plan_of(const gemm_int8_desc &d) {
     return best;
   }
   if (d.N < 4 || kb == 0 || least > 1) return best;
-  // Tiles of 256 x 256, all columns or as many of them as fill rounds of all CUs, the others' tiles in a launch
-  // behind them.  (4096 x 14336 x 4096, 3.5 rounds: all 184 us, three rounds and 256 tiles of 128 x 256 192;
-  // 4096 x 4352 x 4096, 272 tiles: 89, one round and others 66.)
+  // Tiles of 256 x 256: all columns or, where that leaves a last round less than half full, as many of them as
+  // fill rounds of all CUs, and the others' tiles in a launch behind them.  (4096 x 14336 x 4096, 3.5 rounds: all
+  // 184 us, three rounds and 256 tiles of 128 x 256 192; 4096 x 6144 x 4096, 1.5: 90, 91; 6144 x 6144 x 2048, 2.25:
+  // 83, 79; 4096 x 4352 x 4096, 1.06: 89, 66.)
   const int64_t mt = (d.M + kWide - 1) / kWide, nt = (d.N + kWide - 1) / kWide;
   const double fix = wide_fix(d);
   const double all =
-      kLaunch + kWideLast + rounds_of((double)(mt * nt), (double)kb, fix, kWideAlone, kWideFull);
+      kLaunch + kWideOnce + rounds_of((double)(mt * nt), (double)kb, fix, kWideAlone, kWideFull);
   if (all < us) {
     us = all;
     best = {-2, (int32_t)nt, 1, 0, 0, 0};
   }
   const int64_t front = mt * nt / kCUs * kCUs / mt;   // columns of tiles
-  if (front > 0 && front < nt) {
+  if (front > 0 && front < nt && mt * nt % kCUs < kCUs / 2) {
     Int8Plan rest{};
     const double t =
-        kBehind + kWideLast + rounds_of((double)(mt * front), (double)kb, fix, kWideAlone, kWideFull) +
+        kWideOnce + rounds_of((double)(mt * front), (double)kb, fix, kWideAlone, kWideFull) +
         best_tiles(d, d.N - front * kWide, kb, 1, rest);
     if (t < us) {
       best = rest;

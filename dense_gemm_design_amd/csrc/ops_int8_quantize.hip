@@ -3,11 +3,17 @@
 //
 //   s = max(amax / 127, 2^-120),  q = the exact quotient x / s rounded to even
 //
-// Rounding: t = x r + 1.5 2^23 with r near 1 / s leaves the integer next to x / s in t's last bits, and
-// rest = x - q s is exact in fp32 (a multiple of the smaller of x's and s's last places, at most s / 2
-// and a little in size), so |rest| against s / 2 says whether q is the nearest integer, and where it is a
-// tie.  Four instructions a value; what is not right yet, one in some thousands, is mended behind a
-// branch.  (2^-120 as the smallest scale keeps every rest a normal multiple of 2^-149.)
+// Rounding: t = x r + 1.5 2^23 with r near 1 / s leaves an integer next to x / s in t's last bits.  Which one
+// matters next to a border between two, k + 1/2.
+//  * rest = x - q s is exact in fp32 (a multiple of the smaller of x's and s's last places, at most s / 2
+//    and a little in size), so |rest| against s / 2 says whether q is the nearest integer, and where it is a
+//    tie.  fp32 x: four instructions a value; what is not right yet, one in some thousands, is mended
+//    behind a branch.  (2^-120 as the smallest scale keeps every rest a normal multiple of 2^-149.)
+//  * bf16 x: 127 x / amax of 8-bit mantissas is either on a border, which is common enough (x = amax / 2)
+//    that most waves would take that branch, or 2^-16 of itself away from it.  So the rounding of s alone
+//    decides: r is moved by 2^-18 to the side that s was rounded from.  One instruction a value; where s is
+//    exact, a border is a tie, and the values go the other way.  (8192 x 4096, both sides: 49 us with the
+//    first way for all, 
 //
 //  * Rows alone: one pass, a row in the registers of a wave, of four or of sixteen.
 //  * With columns, or rows of over 65536: a first kernel leaves maxima of rows and columns over parts of
@@ -55,40 +61,31 @@ __device__ __forceinline__ float scale_of(uint32_t amax) {
   return fmaxf(float_of(amax) / 127.0f, 0x1p-120f);
 }
 
-// Dividing by one scale.  All codes of a NaN scale are zeros.
+// Dividing by the scale of a row whose largest magnitude has the bits amax: r is negative where the rest of
+// each value has to be looked at, and zero, as all codes are, for a NaN scale.
 struct Divide {
-  float s, r, half;
-  uint32_t keep;
-  __device__ __forceinline__ explicit Divide(float scale) : s(scale) {
-    const bool fine = s == s;
-    r = fine ? __builtin_amdgcn_rcpf(s) : 0.0f;
-    half = 0.5f * s;
-    keep = fine ? ~0u : 0u;
-  }
+  float s, r;
 };
+template <class T>
+__device__ __forceinline__ Divide divide_by(uint32_t amax) {
+  Divide d{scale_of(amax), 0.0f};
+  if (d.s != d.s) return d;
+  d.r = __builtin_amdgcn_rcpf(d.s);
+  if constexpr (sizeof(T) == 2) {
+    const float e = fmaf(-127.0f, d.s, float_of(amax));   // exact
+    if (e == 0.0f || d.s == 0x1p-120f)
+      d.r = -d.r;
+    else
+      d.r *= e > 0.0f ? 1.0f + 0x1p-18f : 1.0f - 0x1p-18f;
+  } else {
+    d.r = -d.r;
+  }
+  return d;
+}
 
 constexpr float kMagic = 0x1.8p23f;
 
-// Eight codes: element i is x(i) divided by d(i).
-template <class GetX, class GetD>
-__device__ __forceinline__ u32x2_t codes8(GetX x, GetD d) {
-  uint32_t t[8];
-  bool off = false;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const float v = fmaf(x(i), d(i).r, kMagic);
-    const float rest = fmaf(kMagic - v, d(i).s, x(i));
-    off |= fabsf(rest) >= d(i).half;
-    t[i] = bits_of(v);
-  }
-  if (off) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float v = float_of(t[i]), rest = fmaf(kMagic - v, d(i).s, x(i));
-      const bool wrong = fabsf(rest) > d(i).half || (fabsf(rest) == d(i).half && (t[i] & 1));
-      if (wrong) t[i] = bits_of(v + (rest > 0.0f ? 1.0f : -1.0f));
-    }
-  }
+__device__ __forceinline__ u32x2_t last_bytes(const uint32_t (&t)[8]) {
   u32x2_t c;
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
@@ -97,6 +94,35 @@ __device__ __forceinline__ u32x2_t codes8(GetX x, GetD d) {
     c[h] = lo | (hi << 16);
   }
   return c;
+}
+// Eight codes: element i is x(i) divided by d.
+template <class T, class GetX>
+__device__ __forceinline__ u32x2_t codes8(GetX x, const Divide &d) {
+  uint32_t t[8];
+  if (sizeof(T) == 2 && d.r >= 0.0f) {   // (a NaN in x, whose low bytes are zeros, stays one)
+#pragma unroll
+    for (int i = 0; i < 8; ++i) t[i] = bits_of(fmaf(x(i), d.r, kMagic));
+    return last_bytes(t);
+  }
+  const float half = 0.5f * d.s;
+  bool off = false;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const float v = fmaf(x(i), -d.r, kMagic);
+    off |= fabsf(fmaf(kMagic - v, d.s, x(i))) >= half;
+    t[i] = bits_of(v);
+  }
+  if (off) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float v = float_of(t[i]), rest = fmaf(kMagic - v, d.s, x(i));
+      const bool wrong = fabsf(rest) > half || (fabsf(rest) == half && (t[i] & 1));
+      if (wrong) t[i] = bits_of(v + (rest > 0.0f ? 1.0f : -1.0f));
+    }
+  }
+  const uint32_t keep = d.s == d.s ? ~0u : 0u;
+  const u32x2_t c = last_bytes(t);
+  return u32x2_t{c[0] & keep, c[1] & keep};
 }
 
 template <class T>
@@ -136,14 +162,13 @@ __global__ void __launch_bounds__(WAVES == 1 ? 256 : WAVES * 64) rows_kernel(con
 #pragma unroll
     for (int w = 0; w < WAVES; ++w) m = max(m, slot[w]);
   }
-  const Divide d(scale_of(m));
+  const Divide d = divide_by<T>(m);
   if (at == 0) a.scales[row] = d.s;
 #pragma unroll
   for (int i = 0; i < V; ++i) {
     const int64_t e = at + i * THREADS * 8;
     if (e >= a.pitch) break;
-    const u32x2_t c = codes8([&](int j) { return v[i].at(j); }, [&](int) { return d; });
-    *(u32x2_t *)(a.codes + row * a.pitch + e) = u32x2_t{c[0] & d.keep, c[1] & d.keep};
+    *(u32x2_t *)(a.codes + row * a.pitch + e) = codes8<T>([&](int j) { return v[i].at(j); }, d);
   }
 }
 
@@ -163,10 +188,9 @@ __global__ void __launch_bounds__(256) parts_kernel(const RowQuantArgs a) {
     for (int i = tid; i < high; i += 256) rmax[i] = 0;
     __syncthreads();
   }
-  const int64_t b0 = (int64_t)pc * a.wide;
-  const int blocks = (int)(a.col_tiles - b0 < a.wide ? a.col_tiles - b0 : a.wide);
-  for (int b = 0; b < blocks; ++b) {
-    const int64_t c0 = (b0 + b) * 128 + cg * 8, nc = a.cols - c0;
+  const int64_t b1 = (int64_t)(pc + 1) * a.wide < a.col_tiles ? (int64_t)(pc + 1) * a.wide : a.col_tiles;
+  for (int64_t b = (int64_t)pc * a.wide; b < b1; ++b) {
+    const int64_t c0 = b * 128 + cg * 8, nc = a.cols - c0;
     uint32_t kmax[8];
 #pragma unroll
     for (int j = 0; j < 8; ++j) kmax[j] = 0;
@@ -202,7 +226,7 @@ __global__ void __launch_bounds__(256) parts_kernel(const RowQuantArgs a) {
         for (int j = 0; j < 8; ++j) cmax[wave][cg * 8 + j] = kmax[j];
       }
       __syncthreads();
-      const int64_t c = (b0 + b) * 128 + tid;
+      const int64_t c = b * 128 + tid;
       if (tid < 128 && c < a.cols)
         a.col_parts[pr * a.cols + c] =
             max(max(cmax[0][tid], cmax[1][tid]), max(cmax[2][tid], cmax[3][tid]));
@@ -221,8 +245,8 @@ __device__ __forceinline__ u32x2_t first_bytes(u32x2_t c, int64_t n) {
   return u32x2_t{c[0] & (uint32_t)keep, c[1] & (uint32_t)(keep >> 32)};
 }
 
-// The scale of element i of `count` from its `parts` maxima.
-__device__ __forceinline__ float scale_of_parts(const uint32_t *p, int parts, int64_t count,
+// The largest of the `parts` maxima of element i of `count`.
+__device__ __forceinline__ uint32_t max_of_parts(const uint32_t *p, int parts, int64_t count,
                                                 int64_t i) {
   uint32_t m = 0;
   for (int k = 0; k < parts; k += 8) {
@@ -232,15 +256,22 @@ __device__ __forceinline__ float scale_of_parts(const uint32_t *p, int parts, in
 #pragma unroll
     for (int j = 0; j < 8; ++j) m = max(m, u[j]);
   }
-  return scale_of(m);
+  return m;
 }
 
 template <class T, bool ROWS, bool COLS>
 __global__ void __launch_bounds__(256) tiles_kernel(const RowQuantArgs a) {
-  __shared__ float sr[128], sc[128];
+  __shared__ Divide dr[128], dc[128];
   __shared__ __align__(16) uint8_t turned[COLS ? 128 * 128 : 16];
   const int tid = threadIdx.x, cg = tid & 15, rg = tid >> 4;
-  const int64_t ct = blockIdx.x % (uint32_t)a.col_tiles, rt = blockIdx.x / (uint32_t)a.col_tiles;
+  // What the parts' kernel read last comes first and, where its parts divide among them, on the same XCD
+  // (workgroup mod 8): part of it is still in that L2.
+  const uint32_t back = gridDim.x - 1 - blockIdx.x;
+  int64_t ct = blockIdx.x % (uint32_t)a.col_tiles, rt = back / (uint32_t)a.col_tiles;
+  if (a.col_tiles % (8 * a.wide) == 0) {
+    const uint32_t j = (uint32_t)ct / 8;
+    ct = (j / a.wide * 8 + (uint32_t)ct % 8) * a.wide + j % a.wide;
+  }
   const int64_t c0 = ct * 128 + cg * 8, r0 = rt * 128 + rg * 8;
   const int64_t nc = a.cols - c0, nr = a.rows - r0;
   Vec8<T> v[8];
@@ -250,25 +281,24 @@ __global__ void __launch_bounds__(256) tiles_kernel(const RowQuantArgs a) {
   if (tid < 128) {
     const int64_t r = rt * 128 + tid;
     if (ROWS && r < a.rows) {
-      const float s = scale_of_parts(a.row_parts, a.parts_r, a.rows, r);
-      sr[tid] = s;
-      if (ct == 0) a.scales[r] = s;
+      const Divide d = divide_by<T>(max_of_parts(a.row_parts, a.parts_r, a.rows, r));
+      dr[tid] = d;
+      if (ct == 0) a.scales[r] = d.s;
     }
   } else {
     const int64_t c = ct * 128 + tid - 128;
     if (COLS && c < a.cols) {
-      const float s = scale_of_parts(a.col_parts, a.parts_c, a.cols, c);
-      sc[tid - 128] = s;
-      if (rt == 0) a.scales_t[c] = s;
+      const Divide d = divide_by<T>(max_of_parts(a.col_parts, a.parts_c, a.cols, c));
+      dc[tid - 128] = d;
+      if (rt == 0) a.scales_t[c] = d.s;
     }
   }
   __syncthreads();
   if constexpr (ROWS) {
 #pragma unroll
     for (int p = 0; p < 8; ++p) {
-      const Divide d(p < nr ? sr[rg * 8 + p] : 1.0f);
-      u32x2_t c = codes8([&](int i) { return v[p].at(i); }, [&](int) { return d; });
-      c = first_bytes(u32x2_t{c[0] & d.keep, c[1] & d.keep}, nc);
+      const u32x2_t c = first_bytes(
+          codes8<T>([&](int i) { return v[p].at(i); }, p < nr ? dr[rg * 8 + p] : Divide{1.0f, 0.0f}), nc);
       if (p < nr && c0 < a.pitch) *(u32x2_t *)(a.codes + (r0 + p) * a.pitch + c0) = c;
     }
   }
@@ -276,9 +306,8 @@ __global__ void __launch_bounds__(256) tiles_kernel(const RowQuantArgs a) {
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       const int col = cg * 8 + j;
-      const Divide d(j < nc ? sc[col] : 1.0f);
-      u32x2_t c = codes8([&](int i) { return v[i].at(j); }, [&](int) { return d; });
-      c = first_bytes(u32x2_t{c[0] & d.keep, c[1] & d.keep}, nr);
+      const u32x2_t c = first_bytes(
+          codes8<T>([&](int i) { return v[i].at(j); }, j < nc ? dc[col] : Divide{1.0f, 0.0f}), nr);
       *(u32x2_t *)&turned[col * 128 + (((rg >> 1) ^ (cg & 7)) << 4) + (rg & 1) * 8] = c;
     }
     __syncthreads();

@@ -561,10 +561,10 @@ constexpr TileKind kTiles[] = {
 };
 constexpr int kWide = 256;                       // of the wide kernel's tiles
 constexpr double kWideAlone = 0.95, kWideFull = 1.37;
-// Its rounds write beside the next one's first step; an fp32 C, and rows that are no multiple of four columns,
-// are written before it.  (4096 x 4096 x 4096 bf16 54.5 us, fp32 64.)
+// Its rounds write beside the next one's first step; rows that are no multiple of four columns are written
+// before it.  (Four rounds, 8192 x 8192 x 2048: bf16 115 us, fp32 145, and 174 on tiles of 192 x 192.)
 double wide_fix(const gemm_int8_desc &d) {
-  return d.dtype_c == GEMM_BF16 && d.N % 4 == 0 ? 3.7 : 13.0;
+  return d.N % 4 != 0 ? 13.0 : d.dtype_c == GEMM_BF16 ? 3.7 : 9.0;
 }
 constexpr double kWideOnce = 6.0;   // us before the first round and behind the last
 constexpr double kLaunch = 2.2, kBytes = 5.0e6;  // us of a launch; bytes a us from memory
@@ -601,15 +601,13 @@ double best_tiles(const gemm_int8_desc &d, int64_t N, int64_t kb, int64_t least,
     // K cut for the tiles that do not fill a round: a launch, and 8 bytes an element and piece
     const int64_t whole = least == 1 ? all / kCUs * kCUs : 0, rest = all - whole;
     if (rest == 0 || (least == 1 && rest > kCUs / 2)) continue;
-    for (int64_t s : {2, 3, 4, 6, 8, 12, 16, 24, 32, 48, 64}) {
-      if (s < least && least > 64) s = least;
-      if (s < least || (s > least && (s * 4 > kb || rest * s > 2 * kCUs))) continue;
+    for (int64_t s : {least, 2l, 3l, 4l, 6l, 8l, 12l, 16l, 24l, 32l, 48l, 64l}) {
+      if (s == 1 || s < least || (s > least && (s * 4 > kb || rest * s > 2 * kCUs))) continue;
       const double items = (double)(rest * s), blocks = (double)((kb + s - 1) / s);
       offer(kLaunch + rounds_of((double)whole, (double)kb, t.fix, t.alone, t.full) +
                 rounds_of(items, blocks, t.fix, t.alone, t.full) + 3.6 +
                 items * (double)(t.bm * t.bn) * 2.8e-6,
             s, whole);
-      if (least > 64) break;
     }
   }
   return us;
@@ -635,7 +633,7 @@ Int8Plan plan_of(const gemm_int8_desc &d) {
       t = t < way ? way : t;
       t = 2.4 + (t < memory ? memory : t);
       if (s > 1) t += 2.4 + (double)(s * d.M * d.N) * 2.8e-6;
-      if (t < us || (best.tiles >= 0 && least > 64)) {
+      if (t < us) {
         us = t;
         best = {-1, 0, (int32_t)s, 1, (int32_t)nt, 0};
       }
@@ -644,9 +642,9 @@ Int8Plan plan_of(const gemm_int8_desc &d) {
   }
   if (d.N < 4 || kb == 0 || least > 1) return best;
   // Tiles of 256 x 256: all columns or, where that leaves a last round less than half full, as many of them as
-  // fill rounds of all CUs, and the others' tiles in a launch behind them.  (4096 x 14336 x 4096, 3.5 rounds: all
-  // 184 us, three rounds and 256 tiles of 128 x 256 192; 4096 x 6144 x 4096, 1.5: 90, 91; 6144 x 6144 x 2048, 2.25:
-  // 83, 79; 4096 x 4352 x 4096, 1.06: 89, 66.)
+  // fill rounds of all CUs, and the others' tiles in a launch behind them.  (4096 x 14336 x 4096, 3.5 rounds:
+  // all 184 us, three rounds and 256 tiles of 128 x 256 192; 4096 x 6144 x 4096, 1.5: 90, 91; 6144 x 6144 x
+  // 2048, 2.25: 83, 79; 4096 x 4352 x 4096, 1.06: 89, 66.)
   const int64_t mt = (d.M + kWide - 1) / kWide, nt = (d.N + kWide - 1) / kWide;
   const double fix = wide_fix(d);
   const double all =
@@ -683,7 +681,9 @@ int check(const gemm_int8_desc *d) {
   // offsets inside a tile of 256 rows (of A, B or C) stay under 31 bits, work-items under 2^32
   if (d->lda > (1 << 22) || d->ldb > (1 << 22)) return GEMM_ERR_UNSUPPORTED;
   if (d->M > (1ll << 31) || d->N > (1ll << 22)) return GEMM_ERR_UNSUPPORTED;
-  if (((d->M + 63) / 64) * ((d->N + 63) / 64) > (1ll << 22)) return GEMM_ERR_UNSUPPORTED;
+  // K that is cut everywhere: those of the kernel that adds the pieces, 256 for 1024 elements of whole tiles
+  const int64_t tiles = ((d->M + 63) / 64) * ((d->N + 63) / 64);
+  if (tiles > (1ll << (d->K > 128ll * kMostBlocks ? 19 : 22))) return GEMM_ERR_UNSUPPORTED;
   return GEMM_OK;
 }
 
@@ -754,7 +754,7 @@ extern "C" int gemm_int8_run(const gemm_int8_desc *d, const void *A, const float
   a.kb = (int32_t)((d->K + 127) / 128);
   a.out_bf16 = d->dtype_c == GEMM_BF16;
   a.src_bf16 = d->dtype_source == GEMM_BF16;
-  a.plain_rows = !source && a.out_bf16 && d->N % 4 == 0 && !((uintptr_t)C & 7);
+  a.plain_rows = !source && d->N % 4 == 0 && !((uintptr_t)C & (a.out_bf16 ? 7 : 15));
   hipStream_t s = (hipStream_t)stream;
   if (p.wide > 0) {
     a.mt = (int32_t)((d->M + kWide - 1) / kWide);

@@ -6,7 +6,7 @@
 // read).  The first two and the last two rows of blocks are taken column by column, so that the reads of
 // B's fragments have 2 FN slots, and as many before their next MFMA.
 //
-// Workgroups stay for tile after tile: the loads of the next one are under way when a tile ends, and a bf16
+// Workgroups stay for tile after tile: the loads of the next one are under way when a tile ends, and a
 // tile that was left in the registers is scaled and written out beside the next one's first step.
 #include "ops_int8.h"
 
@@ -32,12 +32,13 @@ __device__ __forceinline__ bool tile_at(const Int8Args &a, int32_t b, int32_t ro
   return true;
 }
 
-// The bf16 output of a wave's FM x FN blocks of 16 x 16, written out one block at a time: block (f, g) goes as
-// it is into one of two halves of a row of blocks in the wave's LDS (4 KB each, 16-byte chunks swizzled).
+// The output of a wave's FM x FN blocks of 16 x 16, written out one block at a time: block (f, g) goes as it
+// is into one of two halves of a row of blocks in the wave's LDS (4 KB each, 16-byte chunks swizzled).
 // Beside the other half's blocks it comes back as rows, four columns a lane -- so that a lane needs the scales
 // and the bias of eight columns only -- and is scaled, finished and stored.
-template <int FM, int FN>
+template <int FM, int FN, class OUT>
 struct OutRows {
+  static constexpr uint32_t ES = sizeof(OUT);
   static constexpr int HALF = FN / 2;   // blocks of a half
   static_assert(HALF == 4, "a half is 64 columns, 16 lanes of four");
   typedef i32x4 __attribute__((address_space(3))) *p128;
@@ -95,21 +96,22 @@ struct OutRows {
   __device__ __forceinline__ void set(const Int8Args &a, int64_t m0, int64_t n0, int lane) {
     const bool inside = m0 < a.M && n0 < a.N;
     const int64_t origin = inside ? m0 * a.N + n0 : 0;
-    cr = uniform_rsrc(a.C + origin * 2, (a.M * a.N - origin) * 2);
+    cr = uniform_rsrc(a.C + origin * ES, (a.M * a.N - origin) * ES);
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       const int at = (lane & 15) * 4;
       const bool ok = inside && n0 + h * (HALF * 16) + at < a.N;
       st_off[h] =
-          ok ? (uint32_t)(lane >> 4) * ((uint32_t)a.N * 8) + h * (HALF * 32) + at * 2 : kOOB;
+          ok ? (uint32_t)(lane >> 4) * 4 * pitch_of(a) + (h * (HALF * 16) + at) * ES : kOOB;
     }
   }
+  static __device__ __forceinline__ uint32_t pitch_of(const Int8Args &a) { return (uint32_t)a.N * ES; }
   __device__ __forceinline__ void clear(const Int8Args &a) {
     cr = uniform_rsrc(a.C, 0);
     st_off[0] = st_off[1] = 0;
   }
   __device__ __forceinline__ void begin(const Int8Args &a) {
-    pitch = (uint32_t)a.N * 2;
+    pitch = pitch_of(a);
     // keeps the compiler from forming the addresses of all writes ahead of time
     asm volatile("" : "+v"(wa), "+v"(ra));
     asm volatile("" : "+s"(pitch));
@@ -123,10 +125,13 @@ struct OutRows {
     f32x4 x;
 #pragma unroll
     for (int e = 0; e < 4; ++e) x[e] = fmaf((float)t[e] * sa[F][J], sb[H][e], bias[H][e]);
-    const u32x2 w = {pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3])};
     // rows are whole: past M the lane's offset, of its row in it, leaves the range
-    __builtin_amdgcn_raw_buffer_store_b64(w, cr, st_off[H] + (uint32_t)(F * 16 + J) * pitch, 0,
-                                          kNonTemporal);
+    const uint32_t off = st_off[H] + (uint32_t)(F * 16 + J) * pitch;
+    if constexpr (ES == 2)
+      __builtin_amdgcn_raw_buffer_store_b64(
+          u32x2{pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3])}, cr, off, 0, kNonTemporal);
+    else
+      __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, x), cr, off, 0, kNonTemporal);
   }
   // a block's sums to half H, where it is block E
   template <int H, int E>
@@ -166,6 +171,7 @@ struct OutRows {
   }
 };
 
+template <class OUT>
 __global__ void __attribute__((amdgpu_flat_work_group_size(256, 256), amdgpu_waves_per_eu(1, 1)))
 wide_int8_kernel(const Int8Args a) {
   constexpr int BM = 256, BN = 256, NW = 4, WM = BM / 2, WN = BN / 2;
@@ -263,7 +269,7 @@ wide_int8_kernel(const Int8Args a) {
     (read(smem, std::integral_constant<int, 0>(), std::integral_constant<int, E>()), ...);
   }(std::make_integer_sequence<int, FM + FN>());
 
-  OutRows<FM, FN> out;
+  OutRows<FM, FN, OUT> out;
   out.init(a, slice, lane);
 
   // One step.  FIRST of a tile: a block's last sums are taken from its accumulators before they start again.
@@ -311,8 +317,8 @@ wide_int8_kernel(const Int8Args a) {
       if (!any) out.flush(a, acc);
       continue;
     }
-    // An fp32 C, a source, columns that are no multiple of four, or a scale of A that B's has to come before:
-    // the sums go through the wave's LDS, half a row of blocks at a time, the source's next half on its way.
+    // A source, columns that are no multiple of four, or a scale of A that B's has to come before: the sums
+    // go through the wave's LDS, half a row of blocks at a time, the source's next half on its way.
     out.clear(a);
     with_source(a, [&](auto src_c) {
       constexpr int SRC = decltype(src_c)::value, HALF = out.HALF;
@@ -371,7 +377,10 @@ wide_int8_kernel(const Int8Args a) {
 hipError_t launch_int8_wide(const Int8Args &a, hipStream_t s) {
   const int64_t tiles = (int64_t)a.mt * a.nt;
   const dim3 grid((uint32_t)(tiles < kWorkers ? tiles : kWorkers));
-  hipLaunchKernelGGL(wide_int8_kernel, grid, dim3(256), 0, s, a);
+  if (a.out_bf16)
+    hipLaunchKernelGGL((wide_int8_kernel<uint16_t>), grid, dim3(256), 0, s, a);
+  else
+    hipLaunchKernelGGL((wide_int8_kernel<float>), grid, dim3(256), 0, s, a);
   return hipGetLastError();
 }
 

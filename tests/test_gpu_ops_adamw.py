@@ -189,14 +189,17 @@ def test_clipping_on_the_way_is_clipping_before(dev, state):
 
 
 @pytest.mark.parametrize("state", ["e4m3", "f32"])
-@pytest.mark.parametrize("count", [88, 89, 200])
-def test_lists_of_many_tensors(dev, count, state):
+@pytest.mark.parametrize("copies", [False, True])
+@pytest.mark.parametrize("count", [88, 96, 97, 120, 121, 300])
+def test_lists_of_many_tensors(dev, count, copies, state):
     """More tensors than a table holds."""
     g = gen(count)
     sizes = [1 + (i * 37) % 400 for i in range(count)]
     params = [randn(g, n).to(F32 if i % 3 else BF16).to(dev) for i, n in enumerate(sizes)]
     grads = [(randn(g, n) * 1e-2).to(F32 if i % 2 else BF16).to(dev) for i, n in enumerate(sizes)]
-    step_and_check(params, grads, make_state(g, params, state, dev), 11, f"{count} tensors")
+    also = [torch.zeros(n, dtype=BF16, device=dev) if p.dtype == F32 else None
+            for n, p in zip(sizes, params)] if copies else None
+    step_and_check(params, grads, make_state(g, params, state, dev), 11, f"{count} tensors", copies=also)
 
 
 @pytest.mark.parametrize("state", ["e4m3", "f32"])

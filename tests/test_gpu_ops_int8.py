@@ -213,6 +213,16 @@ def test_product_of_long_sums(dev, M, N, K):
     assert abs(float(got[0, 0]) / (float(a.scales[0]) * float(b.scales[0]) * 2.0 ** 14 * K) - 1) < 4 * U
 
 
+def test_product_of_long_sums_and_many_tiles(dev):
+    """K in five pieces, and more tiles than there is room for at six."""
+    M, N, K = 1900, 2000, 540000
+    g = torch.Generator(device=dev).manual_seed(12)
+    a, b = (dg.Int8Scaled(torch.randint(-128, 128, (rows, K), generator=g, device=dev, dtype=torch.int8),
+                          torch.rand(rows, generator=g, device=dev) + 0.5, K) for rows in (M, N))
+    a.data[:40] = b.data[:40] = -128
+    check_product(a, b, F32, "long and many")
+
+
 def test_product_is_the_same_in_every_batch(dev):
     """Sums are exact, and the rest is element by element: a row has the same bits alone and in any batch,
     and a column in any weight."""

@@ -196,6 +196,23 @@ def test_c_abi_refusals():
     assert lib.gemm_adamw_step(None, 0, None, None) == INV
 
 
+def test_long_sums_are_cut_at_any_size():
+    """K past 130944 always goes to int32 pieces of at most that, whatever the number of tiles."""
+    lib = O.load()
+    n = ctypes.c_size_t()
+    for K in (130945, 262144, 540000, 600000, 1000000, 2100000, 3000000, 1 << 22):
+        pieces = -(-K // (1023 * 128))
+        for M, N in ((1, 1), (32, 5000), (33, 64), (300, 300), (1900, 2000), (2048, 2048), (9000, 7000)):
+            d = O.GemmInt8Desc(M=M, N=N, K=K, lda=1 << 22, ldb=1 << 22, dtype_c=2, dtype_source=2)
+            assert lib.gemm_int8_workspace(ctypes.byref(d), ctypes.byref(n)) == 0
+            assert n.value >= pieces * M * N * 4, (M, N, K)
+    # what adds the pieces has a workgroup for 1024 elements, and a launch under 2^32 work-items
+    d = O.GemmInt8Desc(M=1 << 16, N=1 << 16, K=1 << 18, lda=1 << 18, ldb=1 << 18, dtype_c=2, dtype_source=2)
+    assert lib.gemm_int8_workspace(ctypes.byref(d), ctypes.byref(n)) == UNS
+    d.K = d.lda = d.ldb = 1 << 16
+    assert lib.gemm_int8_workspace(ctypes.byref(d), ctypes.byref(n)) == 0 and n.value == 0
+
+
 @pytest.mark.parametrize("count", [2, 40])
 def test_overlaps_in_any_order(count):
     """Tensors in any order of addresses; one that overlaps another anywhere in the list is found."""

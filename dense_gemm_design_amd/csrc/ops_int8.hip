@@ -382,12 +382,19 @@ __device__ __forceinline__ bool item_at(const Int8Args &a, int32_t b, int32_t ro
   return true;
 }
 
-template <int BM, int BN, int S>
+// SHIFTED: rows that do not start at multiples of 128 bytes.  A k-block's 128 bytes of such a row lie in two of
+// memory's lines, and loading both for every block took 1000 x 4104 x 8201 from 40 to 52 us.  So a stage holds
+// a line of each row instead, chunk c of a k-block at the place that it has anyway, and a lane reads it from
+// this stage or, where its row starts `off` chunks behind a line and c + off > 7, from the next.  All rows of
+// a lane start alike: they are 16 apart.  An item has a line more than k-blocks, so a step goes by
+// behind it without a product.
+template <int BM, int BN, int S, bool SHIFTED>
 __global__ void __attribute__((amdgpu_flat_work_group_size(256, 256), amdgpu_waves_per_eu(1, 1)))
 pipe_kernel(const Int8Args a) {
   constexpr int NW = 4, WM = BM / 2, WN = BN / 2, FM = WM / 16, FN = WN / 16, NM = FM * FN;
   constexpr int LA = BM / 8 / NW, LB = BN / 8 / NW, L = LA + LB;
   constexpr int STAGE = (BM + BN) * 128;
+  constexpr int MORE = SHIFTED ? 1 : 0;   // stages that a step reads besides its own
   static_assert(S * STAGE <= 160 * 1024 && (S - 2) * L <= 63, "");
   __shared__ __align__(1024) char smem_[S * STAGE];
   lds_t *const smem = (lds_t *)smem_;
@@ -399,16 +406,23 @@ pipe_kernel(const Int8Args a) {
   int pstage = 0;
   __amdgpu_buffer_rsrc_t ra = uniform_rsrc(a.A, 0), rb = ra;
   const uint32_t row0 = wave * 8 + lane / 8;
-  const uint32_t chunk = ((lane % 8) ^ ((row0 >> 1) & 7)) * 16;
+  const uint32_t spot = (lane % 8) ^ ((row0 >> 1) & 7);   // a chunk of the k-block
+  // where the line's chunk that goes there lies, from the line's k-block on: one before it where a row starts
+  // behind it, which is no chunk of the row, or the one of the block before
+  const auto chunk_at = [&](const char *base, int64_t ld) {
+    const uint32_t off = SHIFTED ? (uint32_t)((uintptr_t)base + row0 * ld) >> 4 & 7 : 0;
+    return (int32_t)((spot + off) % 8 - off) * 16;
+  };
+  const int32_t chunk_a = chunk_at(a.A, a.lda), chunk_b = chunk_at(a.B, a.ldb);
   const uint32_t stepa = NW * 8 * (uint32_t)a.lda, stepb = NW * 8 * (uint32_t)a.ldb;
-  const uint32_t oa = row0 * (uint32_t)a.lda + chunk, ob = row0 * (uint32_t)a.ldb + chunk;
+  const uint32_t oa = row0 * (uint32_t)a.lda + chunk_a, ob = row0 * (uint32_t)a.ldb + chunk_b;
   auto producer_item = [&] {
     Item w;
     if (item_at(a, blockIdx.x, pround, BM, BN, w)) {
       const int32_t rows_a = (int32_t)(a.M - w.m0 < BM ? a.M - w.m0 : BM);
       const int32_t rows_b = (int32_t)(a.N - w.n0 < BN ? a.N - w.n0 : BN);
       pk = w.kb0;
-      pend = w.kb1;
+      pend = w.kb1 + MORE;
       ra = uniform_rsrc(a.A + w.m0 * a.lda, rows_a * a.lda);
       rb = uniform_rsrc(a.B + w.n0 * a.ldb, rows_b * a.ldb);
     } else {   // empty ranges read as zeros
@@ -422,9 +436,8 @@ pipe_kernel(const Int8Args a) {
   lds_t *to;
   auto begin = [&] {
     const uint32_t k = (uint32_t)pk * 128;
-    const bool past = k + chunk >= (uint32_t)a.kbytes;
-    la = past ? kOOB : oa + k;
-    lb = past ? kOOB : ob + k;
+    la = (int32_t)k + chunk_a >= a.kbytes ? kOOB : oa + k;
+    lb = (int32_t)k + chunk_b >= a.kbytes ? kOOB : ob + k;
     to = smem + pstage * STAGE + wave * 1024;
   };
   // load J of the k-block: eight rows of A or of B.  A row past the tile's edge lies past its
@@ -450,15 +463,31 @@ pipe_kernel(const Int8Args a) {
   const uint32_t ck[2] = {(g4 ^ x) * 16, ((g4 + 4) ^ x) * 16};
   const uint32_t arow = (wm * WM + r16) * 128, brow = BM * 128 + (wn * WN + r16) * 128;
   typedef const i32x4 __attribute__((address_space(3))) *frag;
+  // the rows of a lane in A and B whose chunk of a half is in the next stage
+  const auto is_next = [&](const char *base, int64_t ld, int h) {
+    return SHIFTED && g4 + 4 * h + ((uint32_t)((uintptr_t)base + r16 * ld) >> 4 & 7) > 7;
+  };
+  const bool next_a[2] = {is_next(a.A, a.lda, 0), is_next(a.A, a.lda, 1)};
+  const bool next_b[2] = {is_next(a.B, a.ldb, 0), is_next(a.B, a.ldb, 1)};
   i32x4 fa[2][FM], fb[2][FN], acc[FM][FN];
+  const lds_t *at_a[2], *at_b[2];   // of the lane's first row, in each half
+  auto stage_of = [&](auto half_c, int stage, int after) {
+    constexpr int H = decltype(half_c)::value;
+    const lds_t *const st = smem + stage * STAGE, *const more = smem + after * STAGE;
+    at_a[H] = (SHIFTED && next_a[H] ? more : st) + arow + ck[H];
+    at_b[H] = (SHIFTED && next_b[H] ? more : st) + brow + ck[H];
+  };
   // fragment E of a half: B's first
-  auto read = [&](const lds_t *st, auto half_c, auto e_c) {
+  auto read = [&](auto half_c, auto e_c) {
     constexpr int H = decltype(half_c)::value, E = decltype(e_c)::value;
     if constexpr (E < FN)
-      fb[H][E] = *(frag)(st + brow + ck[H] + E * 2048);
+      fb[H][E] = *(frag)(at_b[H] + E * 2048);
     else
-      fa[H][E - FN] = *(frag)(st + arow + ck[H] + (E - FN) * 2048);
+      fa[H][E - FN] = *(frag)(at_a[H] + (E - FN) * 2048);
   };
+  const auto after = [](int stage) { return stage == S - 1 ? 0 : stage + 1; };
+  using FIRST_HALF = std::integral_constant<int, 0>;
+  using OTHER_HALF = std::integral_constant<int, 1>;
   producer_item();
 #pragma unroll
   for (int s = 0; s < S; ++s) {
@@ -468,16 +497,26 @@ pipe_kernel(const Int8Args a) {
     }(std::make_integer_sequence<int, L>());
     end();
   }
-  asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" ::"n"((S - 1) * L < 63 ? (S - 1) * L : 63) : "memory");
-  [&]<int... E>(std::integer_sequence<int, E...>) {
-    (read(smem, std::integral_constant<int, 0>(), std::integral_constant<int, E>()), ...);
-  }(std::make_integer_sequence<int, FM + FN>());
-
+  constexpr int LEFT = (S - 1 - MORE) * L < 63 ? (S - 1 - MORE) * L : 63;
+  asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" ::"n"(LEFT) : "memory");
   int stage = 0;   // of the step
+  auto read_first_half = [&] {
+    stage_of(FIRST_HALF(), stage, after(stage));
+    [&]<int... E>(std::integer_sequence<int, E...>) {
+      (read(FIRST_HALF(), std::integral_constant<int, E>()), ...);
+    }(std::make_integer_sequence<int, FM + FN>());
+  };
+  read_first_half();
+
+  auto handshake = [&] {
+    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"((S - 2 - MORE) * L) : "memory");
+    begin();
+  };
   auto kstep = [&](auto first_c) {
-    const lds_t *const now = smem + stage * STAGE;
-    stage = stage == S - 1 ? 0 : stage + 1;
-    const lds_t *const next = smem + stage * STAGE;
+    const int next = after(stage);
+    stage_of(OTHER_HALF(), stage, next);
+    stage_of(FIRST_HALF(), next, after(next));
+    stage = next;
     // what was moved or made ready between steps is two wait states old before an MFMA reads it
     asm volatile("s_nop 1" ::: "memory");
     int8_step<FM, FN, L>(
@@ -488,12 +527,7 @@ pipe_kernel(const Int8Args a) {
           else
             mfma_int8_inplace(acc[f][g], fb[H][g], fa[H][f]);
         },
-        [&](auto half_c, auto e_c) { read(decltype(half_c)::value ? now : next, half_c, e_c); },
-        [&] {
-          asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"((S - 2) * L) : "memory");
-          begin();
-        },
-        load);
+        read, handshake, load);
     end();
   };
   Item w;
@@ -501,6 +535,15 @@ pipe_kernel(const Int8Args a) {
     kstep(std::true_type());
     for (int32_t kb = w.kb0 + 1; kb < w.kb1; ++kb) kstep(std::false_type());
     mfma_wait_states();
+    if constexpr (SHIFTED) {
+      handshake();
+      [&]<int... J>(std::integer_sequence<int, J...>) {
+        (load(std::integral_constant<int, J>()), ...);
+      }(std::make_integer_sequence<int, L>());
+      end();
+      stage = after(stage);
+      read_first_half();
+    }
     write_blocks<BM, BN, FM, FN>(a, w.piece, w.m0, w.n0, wm * WM + r16, wn * WN + g4 * 4,
                                  [&](int f, int g) {
                                    return i32x4{acc_read(acc[f][g][0]), acc_read(acc[f][g][1]),
@@ -531,10 +574,12 @@ __global__ void __launch_bounds__(256) join_tiles_kernel(const Int8Args a) {
 // and, for each k-block, `alone` where few CUs are at work to `full` where all are, which then share the way
 // to the caches and the power.  (At 4096 x 4096, rows against us by each kernel, smallest tile to largest:
 // 64: 10.2, 14.1, 17.1; 256: 11.5, 14.4, 18.0; 512: 20, 15.7, 18.3; 1024: 36, 27, 22.0, 24.8, 30.4, 28.6, 47;
-// 2048: 71, 55, 40, 46, 36, 34.8, 47.)
+// 2048: 71, 55, 40, 46, 36, 34.8, 47.  `shifted`: 1000 x 4104 x 8192 and x 8201: 64, 71 on 64 x 128; 58, 64; 42,
+// 45; 42, 45; 51, 57; 48, 60; 48, 60.)
 struct TileKind {
   int32_t bm, bn;
   double fix, alone, full;
+  double shifted;   // times a k-block's, where rows do not start at multiples of 128 bytes
   void (*launch)(const Int8Args &, hipStream_t);
 };
 template <int BM, int BN, int WGM, int WGN, int KG, int S>
@@ -546,21 +591,25 @@ void launch_tiles(const Int8Args &a, hipStream_t s) {
 template <int BM, int BN, int S>
 void launch_pipe(const Int8Args &a, hipStream_t s) {
   const int64_t items = a.whole + (int64_t)(a.mt * a.nt - a.whole) * a.splits;
-  hipLaunchKernelGGL((pipe_kernel<BM, BN, S>), dim3((uint32_t)(items < kCUs ? items : kCUs)), dim3(256), 0,
-                     s, a);
+  const dim3 grid((uint32_t)(items < kCUs ? items : kCUs));
+  if (((uintptr_t)a.A | (uintptr_t)a.B | (uintptr_t)a.lda | (uintptr_t)a.ldb) % 128)
+    hipLaunchKernelGGL((pipe_kernel<BM, BN, S, true>), grid, dim3(256), 0, s, a);
+  else
+    hipLaunchKernelGGL((pipe_kernel<BM, BN, S, false>), grid, dim3(256), 0, s, a);
 }
 constexpr TileKind kTiles[] = {
-    {64, 64, 1.2, 0.185, 0.245, launch_tiles<64, 64, 2, 2, 2, 8>},
-    {64, 128, 2.0, 0.32, 0.36, launch_pipe<64, 128, 5>},
-    {128, 128, 3.2, 0.385, 0.51, launch_pipe<128, 128, 4>},
-    {128, 192, 3.8, 0.52, 0.64, launch_pipe<128, 192, 4>},
-    {192, 128, 3.8, 0.52, 0.64, launch_pipe<192, 128, 4>},
-    {192, 192, 4.5, 0.70, 0.93, launch_pipe<192, 192, 3>},
-    {128, 256, 4.6, 0.64, 0.88, launch_pipe<128, 256, 3>},
-    {256, 128, 4.6, 0.64, 0.88, launch_pipe<256, 128, 3>},
+    {64, 64, 1.2, 0.185, 0.245, 1.25, launch_tiles<64, 64, 2, 2, 2, 8>},
+    {64, 128, 2.0, 0.32, 0.36, 1.1, launch_pipe<64, 128, 5>},
+    {128, 128, 3.2, 0.385, 0.51, 1.08, launch_pipe<128, 128, 4>},
+    {128, 192, 3.8, 0.52, 0.64, 1.1, launch_pipe<128, 192, 4>},
+    {192, 128, 3.8, 0.52, 0.64, 1.1, launch_pipe<192, 128, 4>},
+    {192, 192, 4.5, 0.70, 0.93, 1.13, launch_pipe<192, 192, 3>},
+    {128, 256, 4.6, 0.64, 0.88, 1.27, launch_pipe<128, 256, 3>},
+    {256, 128, 4.6, 0.64, 0.88, 1.27, launch_pipe<256, 128, 3>},
 };
 constexpr int kWide = 256;                       // of the wide kernel's tiles
-constexpr double kWideAlone = 0.95, kWideFull = 1.37;
+constexpr double kWideAlone = 0.95, kWideFull = 1.37, kWideShifted = 1.25;
+bool is_shifted(const gemm_int8_desc &d) { return (d.lda | d.ldb) % 128 != 0; }
 // Its rounds write beside the next one's first step; rows that are no multiple of four columns are written
 // before it.  (Four rounds, 8192 x 8192 x 2048: bf16 115 us, fp32 145, and 174 on tiles of 192 x 192.)
 double wide_fix(const gemm_int8_desc &d) {
@@ -586,7 +635,11 @@ double rounds_of(double items, double blocks, double fix, double alone, double f
 double best_tiles(const gemm_int8_desc &d, int64_t N, int64_t kb, int64_t least, Int8Plan &best) {
   double us = 1e30;
   for (int k = 0; k < (int)(sizeof(kTiles) / sizeof(kTiles[0])); ++k) {
-    const TileKind &t = kTiles[k];
+    TileKind t = kTiles[k];
+    if (is_shifted(d)) {
+      t.alone *= t.shifted;
+      t.full *= t.shifted;
+    }
     const int64_t mt = (d.M + t.bm - 1) / t.bm, nt = (N + t.bn - 1) / t.bn, all = mt * nt;
     const auto offer = [&](double time, int64_t splits, int64_t whole) {
       if (time >= us) return;
@@ -646,9 +699,10 @@ Int8Plan plan_of(const gemm_int8_desc &d) {
   // all 184 us, three rounds and 256 tiles of 128 x 256 192; 4096 x 6144 x 4096, 1.5: 90, 91; 6144 x 6144 x
   // 2048, 2.25: 83, 79; 4096 x 4352 x 4096, 1.06: 89, 66.)
   const int64_t mt = (d.M + kWide - 1) / kWide, nt = (d.N + kWide - 1) / kWide;
-  const double fix = wide_fix(d);
+  const double fix = wide_fix(d), times = is_shifted(d) ? kWideShifted : 1.0;
+  const double alone = kWideAlone * times, full = kWideFull * times;
   const double all =
-      kLaunch + kWideOnce + rounds_of((double)(mt * nt), (double)kb, fix, kWideAlone, kWideFull);
+      kLaunch + kWideOnce + rounds_of((double)(mt * nt), (double)kb, fix, alone, full);
   if (all < us) {
     us = all;
     best = {-2, (int32_t)nt, 1, 0, 0, 0};
@@ -657,7 +711,7 @@ Int8Plan plan_of(const gemm_int8_desc &d) {
   if (front > 0 && front < nt && mt * nt % kCUs < kCUs / 2) {
     Int8Plan rest{};
     const double t =
-        kWideOnce + rounds_of((double)(mt * front), (double)kb, fix, kWideAlone, kWideFull) +
+        kWideOnce + rounds_of((double)(mt * front), (double)kb, fix, alone, full) +
         best_tiles(d, d.N - front * kWide, kb, 1, rest);
     if (t < us) {
       best = rest;

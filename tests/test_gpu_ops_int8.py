@@ -301,6 +301,36 @@ def test_product_of_wider_storage(dev, M, N, K):
     assert bool((out[0] == 3).all()) and bool((out[-1] == 3).all())
 
 
+@pytest.mark.parametrize("M,N,K", [(20, 300, 500), (60, 500, 300), (1000, 2000, 1000), (2048, 2048, 700),
+                                   (2000, 3000, 500), (3000, 2000, 500), (3000, 3000, 500), (4500, 2200, 400),
+                                   (3000, 5000, 700), (1000, 1000, 20000), (700, 700, 30000),
+                                   (700, 1000, 140000), (4096, 4096, 200)])
+def test_product_of_rows_that_start_anywhere(dev, M, N, K):
+    """Rows start at every multiple of 16 bytes from a line of memory on, in A and B alike or not; what
+    lies before and behind them are the largest codes."""
+    g = torch.Generator(device=dev).manual_seed(K)
+    scales = [torch.rand(rows, generator=g, device=dev) + 0.5 for rows in (M, N)]
+    data = [torch.randint(-127, 128, (rows, K), generator=g, device=dev, dtype=torch.int8) for rows in (M, N)]
+
+    def held(i, start, pitch):
+        rows, width = data[i].shape[0], R.up(K, 16) * 16
+        flat = torch.full((start + rows * pitch + 64,), 127, dtype=torch.int8, device=dev)
+        view = flat[start:].as_strided((rows, width), (pitch, 1))
+        view[:, :K] = data[i]
+        view[:, K:] = 0
+        return dg.Int8Scaled(view, scales[i], K)
+
+    even = R.up(K, 128) * 128
+    want = dg.int8_gemm(held(0, 0, even), held(1, 0, even), out_dtype="f32")
+    exact = torch.mm(data[0][:50].double(), data[1].double().t().contiguous())
+    exact = exact * scales[0][:50].double()[:, None] * scales[1].double()
+    R.within(want[:50], exact.cpu(), exact.cpu().abs() * 3 * U, "on lines")
+    for start_a, more_a, start_b, more_b in ((0, 16, 0, 16), (16, 16, 112, 48), (96, 112, 32, 112), (64, 64, 0, 0),
+                                             (0, 0, 48, 80), (112, 0, 112, 0), (80, 32, 16, 96)):
+        got = dg.int8_gemm(held(0, start_a, even + more_a), held(1, start_b, even + more_b), out_dtype="f32")
+        assert torch.equal(got, want), (start_a, more_a, start_b, more_b)
+
+
 def test_product_overlaps_are_refused(dev):
     g = gen(15)
     a, b = operand(g, 40, 300, dev), operand(g, 24, 300, dev)

@@ -13,7 +13,7 @@
 //    that most waves would take that branch, or 2^-16 of itself away from it.  So the rounding of s alone
 //    decides: r is moved by 2^-18 to the side that s was rounded from.  One instruction a value; where s is
 //    exact, a border is a tie, and the values go the other way.  (8192 x 4096, both sides: the second kernel
-//    31.6 us, 36.6 with the first way for all.)
+//    takes 28 us, and 5 more with the first way for all.)
 //
 //  * Rows alone: one pass, a row in the registers of a wave, of four or of sixteen.
 //  * With columns, or rows of over 65536: a first kernel leaves maxima of rows and columns over parts of
@@ -41,6 +41,14 @@ struct RowQuantArgs {
   int32_t wide, high;                // of a part: blocks of 128 columns, and rows
   int32_t col_tiles;
 };
+
+template <bool ONCE, class V>
+__device__ __forceinline__ void put(V *p, V v) {   // ONCE: past the caches
+  if constexpr (ONCE)
+    __builtin_nontemporal_store(v, p);
+  else
+    *p = v;
+}
 
 // Largest over the 16 lanes of a DPP row, in each of them.
 __device__ __forceinline__ uint32_t row16_max(uint32_t v) {
@@ -194,7 +202,7 @@ __global__ void __launch_bounds__(256) parts_kernel(const RowQuantArgs a) {
     uint32_t kmax[8];
 #pragma unroll
     for (int j = 0; j < 8; ++j) kmax[j] = 0;
-    constexpr int AHEAD = 8;   // rows of a lane whose loads are in flight together
+    constexpr int AHEAD = 4;   // rows of a lane whose loads are in flight together
     for (int i0 = rg; i0 < high; i0 += 16 * AHEAD) {
       Vec8<T> v[AHEAD];
 #pragma unroll
@@ -259,7 +267,7 @@ __device__ __forceinline__ uint32_t max_of_parts(const uint32_t *p, int parts, i
   return m;
 }
 
-template <class T, bool ROWS, bool COLS>
+template <class T, bool ROWS, bool COLS, bool ONCE>
 __global__ void __launch_bounds__(256) tiles_kernel(const RowQuantArgs a) {
   __shared__ Divide dr[128], dc[128];
   __shared__ __align__(16) uint8_t turned[COLS ? 128 * 128 : 16];
@@ -299,7 +307,7 @@ __global__ void __launch_bounds__(256) tiles_kernel(const RowQuantArgs a) {
     for (int p = 0; p < 8; ++p) {
       const u32x2_t c = first_bytes(
           codes8<T>([&](int i) { return v[p].at(i); }, p < nr ? dr[rg * 8 + p] : Divide{1.0f, 0.0f}), nc);
-      if (p < nr && c0 < a.pitch) *(u32x2_t *)(a.codes + (r0 + p) * a.pitch + c0) = c;
+      if (p < nr && c0 < a.pitch) put<ONCE>((u32x2_t *)(a.codes + (r0 + p) * a.pitch + c0), c);
     }
   }
   if constexpr (COLS) {
@@ -316,7 +324,7 @@ __global__ void __launch_bounds__(256) tiles_kernel(const RowQuantArgs a) {
       const int col = i * 32 + (tid >> 3), chunk = tid & 7;
       const u32x4_t w = *(const u32x4_t *)&turned[col * 128 + ((chunk ^ ((col >> 3) & 7)) << 4)];
       const int64_t row_t = ct * 128 + col, at = rt * 128 + chunk * 16;
-      if (row_t < a.cols && at < a.pitch_t) *(u32x4_t *)(a.codes_t + row_t * a.pitch_t + at) = w;
+      if (row_t < a.cols && at < a.pitch_t) put<ONCE>((u32x4_t *)(a.codes_t + row_t * a.pitch_t + at), w);
     }
   }
 }
@@ -325,6 +333,10 @@ __global__ void __launch_bounds__(256) tiles_kernel(const RowQuantArgs a) {
 
 constexpr int64_t kMostInRow = 65536;   // columns that sixteen waves hold, eight vectors a lane
 
+// Elements from which on the tiles' codes go past the caches, which x then has for itself.  (us so and not:
+// 8192 x 4096 bf16, both sides 42, 45; 4096 x 4096 22.6, 25.2; 3001 x 3001 fp32 26.7, 28.0; 2048 x 4096 bf16
+// alike.)
+constexpr int64_t kPassing = 8 << 20;
 template <class T>
 void launch_rows(const RowQuantArgs &a, hipStream_t s) {
   const dim3 grid((uint32_t)a.rows), four((uint32_t)((a.rows + 3) / 4));
@@ -355,7 +367,10 @@ void launch_parts(const RowQuantArgs &a, hipStream_t s) {
   const uint32_t parts = (uint32_t)a.parts_r * (uint32_t)a.parts_c;
   const uint32_t tiles = (uint32_t)((a.rows + 127) / 128) * (uint32_t)a.col_tiles;
   hipLaunchKernelGGL((parts_kernel<T, ROWS, COLS>), dim3(parts), dim3(256), 0, s, a);
-  hipLaunchKernelGGL((tiles_kernel<T, ROWS, COLS>), dim3(tiles), dim3(256), 0, s, a);
+  if (a.rows * a.cols >= kPassing)
+    hipLaunchKernelGGL((tiles_kernel<T, ROWS, COLS, true>), dim3(tiles), dim3(256), 0, s, a);
+  else
+    hipLaunchKernelGGL((tiles_kernel<T, ROWS, COLS, false>), dim3(tiles), dim3(256), 0, s, a);
 }
 template <class T>
 void launch(const RowQuantArgs &a, hipStream_t s) {

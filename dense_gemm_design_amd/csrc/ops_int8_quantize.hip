@@ -16,12 +16,14 @@
 //    takes 28 us, and 5 more with the first way for all.)
 //
 //  * Rows alone: one pass, a row in the registers of a wave, of four or of sixteen.
-//  * With columns, or rows of over 65536: a first kernel leaves maxima of rows and columns over parts of
+//  * Columns of up to 2048 rows: strips of columns with all their rows in a workgroup's registers, one launch;
+//    with both sides, other workgroups of it take the rows, which they read by themselves.
+//  * Columns of more, or rows of over 65536: a first kernel leaves maxima of rows and columns over parts of
 //    x, at most 16 of a row and some 64 of a column; the second one's workgroups, 128 x 128 elements
 //    each, take the largest of their rows' and columns' parts themselves.  It reads x again, from the
 //    memory-side cache of 256 MB where x fits.
 //
-// Bound by memory.
+// Bound by memory, small ones by a launch and their trips to it.
 #include "../../include/gemm_ops.h"
 #include "ops_common.h"
 
@@ -40,6 +42,7 @@ struct RowQuantArgs {
   int32_t parts_r, parts_c;
   int32_t wide, high;                // of a part: blocks of 128 columns, and rows
   int32_t col_tiles;
+  int32_t groups;                    // of eight columns a strip
 };
 
 template <bool ONCE, class V>
@@ -140,23 +143,31 @@ __device__ __forceinline__ uint32_t largest(const Vec8<T> &v, uint32_t m) {
   return m;
 }
 
+// The bytes of the first n of eight codes; what lies past the matrix is stored as zeros.
+__device__ __forceinline__ u32x2_t first_bytes(u32x2_t c, int64_t n) {
+  if (n >= 8) return c;
+  const uint64_t keep = n <= 0 ? 0 : ~0ull >> (64 - 8 * n);
+  return u32x2_t{c[0] & (uint32_t)keep, c[1] & (uint32_t)(keep >> 32)};
+}
+
 // ---- rows alone -------------------------------------------------------------------------------
 
-// WAVES of a row; four rows a workgroup where that is one.  V vectors of eight a lane.
-template <class T, int WAVES, int V>
-__global__ void __launch_bounds__(WAVES == 1 ? 256 : WAVES * 64) rows_kernel(const RowQuantArgs a) {
+// ROWS rows of a workgroup with WAVES each, from `row0` on, V vectors of eight a lane.
+template <class T, int ROWS, int WAVES, int V>
+__device__ __forceinline__ void quantize_rows(const RowQuantArgs &a, int64_t row0) {
   constexpr int THREADS = WAVES * 64;
-  __shared__ uint32_t slot[WAVES];
-  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
-  const int64_t row = WAVES == 1 ? (int64_t)blockIdx.x * 4 + wave : blockIdx.x;
+  __shared__ uint32_t slot[ROWS * WAVES];
+  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, sub = ROWS > 1 ? wave / WAVES : 0;
+  const int64_t row = row0 + sub;
   if (WAVES == 1 && row >= a.rows) return;
-  const int at = (WAVES == 1 ? lane : (int)threadIdx.x) * 8;
+  const bool there = ROWS == 1 || row < a.rows;
+  const int at = ((int)threadIdx.x - sub * THREADS) * 8;
   const T *const x = (const T *)a.x + row * a.stride;
   Vec8<T> v[V];
 #pragma unroll
   for (int i = 0; i < V; ++i) {
     const int64_t e = at + i * THREADS * 8;
-    load8(v[i], x + e, a.cols - e);
+    load8(v[i], x + e, there ? a.cols - e : 0);
   }
   uint32_t m = 0;
 #pragma unroll
@@ -167,8 +178,9 @@ __global__ void __launch_bounds__(WAVES == 1 ? 256 : WAVES * 64) rows_kernel(con
   if constexpr (WAVES > 1) {
     if (lane == 0) slot[wave] = m;
     __syncthreads();
+    if (!there) return;
 #pragma unroll
-    for (int w = 0; w < WAVES; ++w) m = max(m, slot[w]);
+    for (int w = 0; w < WAVES; ++w) m = max(m, slot[sub * WAVES + w]);
   }
   const Divide d = divide_by<T>(m);
   if (at == 0) a.scales[row] = d.s;
@@ -177,6 +189,67 @@ __global__ void __launch_bounds__(WAVES == 1 ? 256 : WAVES * 64) rows_kernel(con
     const int64_t e = at + i * THREADS * 8;
     if (e >= a.pitch) break;
     *(u32x2_t *)(a.codes + row * a.pitch + e) = codes8<T>([&](int j) { return v[i].at(j); }, d);
+  }
+}
+
+template <class T, int WAVES, int V>
+__global__ void __launch_bounds__(WAVES == 1 ? 256 : WAVES * 64) rows_kernel(const RowQuantArgs a) {
+  constexpr int ROWS = WAVES == 1 ? 4 : 1;
+  quantize_rows<T, ROWS, WAVES, V>(a, (int64_t)blockIdx.x * ROWS);
+}
+
+// ---- columns of few rows --------------------------------------------------------------------------
+
+// A workgroup takes 8 `groups` neighbouring columns with all their rows, a lane eight by eight of them.  ROWS: the
+// workgroups behind take rows, four waves each, which they read by themselves.
+template <class T, int THREADS, bool ROWS>
+__global__ void __launch_bounds__(THREADS) strips_kernel(const RowQuantArgs a) {
+  constexpr int WAVES = THREADS / 64;
+  __shared__ uint32_t cmax[WAVES][128];
+  __shared__ Divide dc[128];
+  const int64_t strips = (a.cols + 8 * a.groups - 1) / (8 * a.groups);
+  if (ROWS && blockIdx.x >= strips) {
+    quantize_rows<T, WAVES / 4, 4, 8>(a, (blockIdx.x - strips) * (WAVES / 4));
+    return;
+  }
+  const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63;
+  const int cg = tid & (a.groups - 1), rg = tid / a.groups;
+  const int64_t c0 = ((int64_t)blockIdx.x * a.groups + cg) * 8, r0 = rg * 8;
+  const int64_t nc = a.cols - c0, nr = a.rows - r0;
+  Vec8<T> v[8];
+#pragma unroll
+  for (int p = 0; p < 8; ++p)
+    load8(v[p], (const T *)a.x + (r0 + p) * a.stride + c0, p < nr ? nc : 0);
+  uint32_t kmax[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    kmax[j] = 0;
+#pragma unroll
+    for (int p = 0; p < 8; ++p) kmax[j] = max(kmax[j], bits_of(v[p].at(j)) & 0x7FFFFFFFu);
+  }
+  for (int o = 32; o >= a.groups; o >>= 1)
+#pragma unroll
+    for (int j = 0; j < 8; ++j) kmax[j] = max(kmax[j], (uint32_t)__shfl_xor((int)kmax[j], o, 64));
+  if (lane < a.groups) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) cmax[wave][cg * 8 + j] = kmax[j];
+  }
+  __syncthreads();
+  if (tid < 8 * a.groups) {
+    uint32_t m = 0;
+#pragma unroll
+    for (int w = 0; w < WAVES; ++w) m = max(m, cmax[w][tid]);
+    dc[tid] = divide_by<T>(m);
+    const int64_t c = (int64_t)blockIdx.x * a.groups * 8 + tid;
+    if (c < a.cols) a.scales_t[c] = dc[tid].s;
+  }
+  __syncthreads();
+  if (r0 >= a.pitch_t) return;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    if (j >= nc) break;
+    const u32x2_t c = codes8<T>([&](int i) { return v[i].at(j); }, dc[cg * 8 + j]);
+    *(u32x2_t *)(a.codes_t + (c0 + j) * a.pitch_t + r0) = first_bytes(c, nr);
   }
 }
 
@@ -244,13 +317,6 @@ __global__ void __launch_bounds__(256) parts_kernel(const RowQuantArgs a) {
     __syncthreads();
     for (int i = tid; i < high; i += 256) a.row_parts[pc * a.rows + r0 + i] = rmax[i];
   }
-}
-
-// The bytes of the first n of eight codes; what lies past the matrix is stored as zeros.
-__device__ __forceinline__ u32x2_t first_bytes(u32x2_t c, int64_t n) {
-  if (n >= 8) return c;
-  const uint64_t keep = n <= 0 ? 0 : ~0ull >> (64 - 8 * n);
-  return u32x2_t{c[0] & (uint32_t)keep, c[1] & (uint32_t)(keep >> 32)};
 }
 
 // The largest of the `parts` maxima of element i of `count`.
@@ -372,9 +438,43 @@ void launch_parts(const RowQuantArgs &a, hipStream_t s) {
   else
     hipLaunchKernelGGL((tiles_kernel<T, ROWS, COLS, false>), dim3(tiles), dim3(256), 0, s, a);
 }
+// Columns in strips where a workgroup has room for all rows; 0: not in strips.  (us in strips and on tiles: 2 x
+// 20564 bf16, columns, 5.8, 16.5; 300 x 9000 bf16, both sides, 9.6, 17.3; 1024 x 4096 10.3, 14.8; 512 x 16384 16.4,
+// 21.6; 2048 x 4096 16.9, 16.5.  Four waves or sixteen: 600 x 600 5.2, 6.8, 300 x 40000 13.6, 15.0, 1000 x
+// 8192 19, 14.)
+struct Strip {
+  int threads, groups;
+};
+Strip strip_of(int64_t rows, int64_t cols, bool rows_side, bool cols_side) {
+  const int64_t high = (rows + 15) / 16 * 16;   // a lane has eight of them
+  if (!cols_side || high > 2048 || cols > (rows_side ? kMostInRow : 1 << 22)) return {0, 0};
+  const int threads = high <= 512 || (high <= 1024 && cols <= 2048) ? 256 : 1024;
+  int groups = 16;
+  while (threads / groups * 8 < high) groups /= 2;
+  while (groups > 2 && cols < 8 * groups * 128) groups /= 2;   // 128 workgroups where there is room
+  return {threads, groups};
+}
+constexpr int64_t kMostWithStrips = 16384;   // columns of a row that four waves hold, eight vectors a lane
+
+template <class T, int THREADS, bool ROWS>
+void launch_strips(const RowQuantArgs &a, hipStream_t s) {
+  const int64_t strips = (a.cols + 8 * a.groups - 1) / (8 * a.groups);
+  const int64_t rows = ROWS ? (a.rows + THREADS / 256 - 1) / (THREADS / 256) : 0;
+  hipLaunchKernelGGL((strips_kernel<T, THREADS, ROWS>), dim3((uint32_t)(strips + rows)), dim3(THREADS), 0, s,
+                     a);
+}
+
 template <class T>
-void launch(const RowQuantArgs &a, hipStream_t s) {
-  if (!a.codes_t && a.cols <= kMostInRow)
+void launch(RowQuantArgs a, hipStream_t s) {
+  const Strip strip = strip_of(a.rows, a.cols, a.codes, a.codes_t);
+  const bool together = a.codes && a.cols <= kMostWithStrips;
+  a.groups = strip.groups;
+  if (strip.threads && a.codes && !together) launch_rows<T>(a, s);
+  if (strip.threads == 256)
+    together ? launch_strips<T, 256, true>(a, s) : launch_strips<T, 256, false>(a, s);
+  else if (strip.threads)
+    together ? launch_strips<T, 1024, true>(a, s) : launch_strips<T, 1024, false>(a, s);
+  else if (!a.codes_t && a.cols <= kMostInRow)
     launch_rows<T>(a, s);
   else if (!a.codes_t)
     launch_parts<T, true, false>(a, s);
@@ -390,7 +490,7 @@ struct Parts {
 };
 Parts parts_of(int64_t rows, int64_t cols, bool rows_side, bool cols_side) {
   Parts p{};
-  if (!cols_side && cols <= kMostInRow) return p;
+  if ((!cols_side && cols <= kMostInRow) || strip_of(rows, cols, rows_side, cols_side).threads) return p;
   const int64_t ct = (cols + 127) / 128;
   p.wide = (int32_t)((ct + 15) / 16);
   p.parts_r = (int32_t)((ct + p.wide - 1) / p.wide);

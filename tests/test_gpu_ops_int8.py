@@ -51,7 +51,9 @@ def check_quantize(x_dev, side, what):
 @pytest.mark.parametrize("rows,cols", [(1, 1), (1, 64), (2, 200), (127, 129), (128, 128), (130, 16),
                                        (300, 257), (515, 1000), (3, 1025), (5, 2049), (9, 4097),
                                        (2, 9000), (3, 17000), (2, 40001), (1, 65536), (2, 65537),
-                                       (3, 70001), (5000, 24), (9000, 130), (70, 20000)])
+                                       (3, 70001), (5000, 24), (9000, 130), (70, 20000), (2049, 130),
+                                       (2048, 40), (2047, 2100), (1024, 4000), (1009, 60), (513, 17),
+                                       (512, 300), (511, 2050), (3000, 3001), (6000, 1500)])
 def test_quantize(dev, rows, cols, dtype):
     print(f"int8 quantize {rows}x{cols} {dtype}", flush=True)
     g = gen(rows * 1000 + cols)
@@ -60,12 +62,12 @@ def test_quantize(dev, rows, cols, dtype):
         check_quantize(x, side, f"{rows}x{cols} side {side}")
 
 
-@pytest.mark.parametrize("cols", [300, 1500, 9000])
+@pytest.mark.parametrize("rows,cols", [(60, 300), (60, 1500), (60, 9000), (600, 300), (1500, 300), (2200, 300)])
 @pytest.mark.parametrize("dtype", TYPES, ids=NAMES)
-def test_quantize_values_at_the_edges(dev, dtype, cols):
+def test_quantize_values_at_the_edges(dev, dtype, rows, cols):
     """Zeros, infinities, NaN, the smallest and largest magnitudes, ties and what lies next to them."""
     g = gen(5)
-    x = randn(g, 60, cols)
+    x = randn(g, rows, cols)
     x[0] = 0
     x[1, 130] = float("inf")
     x[2, 5] = float("nan")
@@ -100,12 +102,15 @@ def test_quantize_ties_at_any_scale(dev, dtype):
     x = torch.cat([x, amax.float(), -amax.float() / 2], dim=1).to(dtype)
     check_quantize(x.to(dev), False, "ties")
     check_quantize(x.t().contiguous().to(dev), True, "ties, transposed")
+    check_quantize(x.t().repeat(4, 1).to(dev), True, "ties, transposed, in sixteen waves")
+    check_quantize(x.t().repeat(9, 1).to(dev), True, "ties, transposed, in tiles")
 
 
 @pytest.mark.parametrize("dtype", TYPES, ids=NAMES)
 def test_quantize_strided_rows(dev, dtype):
-    big = randn(gen(7), 200, 413).to(dtype).to(dev)
-    for view in (big[:, 1:301], big[3:133:2, 7:408], big[:1, 5:9].expand(150, 4)):
+    big = randn(gen(7), 2500, 413).to(dtype).to(dev)
+    for view in (big[:200, 1:301], big[3:133:2, 7:408], big[:1, 5:9].expand(150, 4), big[:, 1:301],
+                 big[:1500, 3:400], big[:1, 5:9].expand(2300, 4)):
         for side in (False, True, "both"):
             check_quantize(view, side, f"stride {view.stride()} {side}")
 

@@ -135,13 +135,14 @@ def test_c_abi_refusals():
                      (dict(pitch=200), INV), (dict(pitch=224), INV), (dict(pitch=192), INV),
                      (dict(pitch_t=16), INV), (dict(x=P + 2), ALI), (dict(codes=P + 8), ALI),
                      (dict(codes_t=P + 8), ALI), (dict(scales=P + 2), ALI), (dict(ws=P + 2), ALI),
-                     (dict(ws=None), WSP), (dict(n=100), WSP), (dict(rows=0), 0), (dict(cols=0), 0),
+                     (dict(rows=3000, pitch_t=3008, ws=None), WSP),
+                     (dict(rows=3000, pitch_t=3008, n=100), WSP), (dict(rows=0), 0), (dict(cols=0), 0),
                      (dict(rows=1 << 31, cols=1 << 31, stride=1 << 31), UNS),
                      (dict(rows=1 << 23, codes_t=None, pitch=208), UNS)):
         assert quant(**kw) == want, kw
     n = ctypes.c_size_t()
     assert lib.gemm_int8_quantize_workspace(30, 200, 1, 0, ctypes.byref(n)) == 0 and n.value == 0
-    assert lib.gemm_int8_quantize_workspace(30, 200, 1, 1, ctypes.byref(n)) == 0 and n.value > 0
+    assert lib.gemm_int8_quantize_workspace(3000, 200, 1, 1, ctypes.byref(n)) == 0 and n.value > 0
     assert lib.gemm_int8_quantize_workspace(30, 200, 0, 0, ctypes.byref(n)) == INV
     assert lib.gemm_int8_quantize_workspace(30, 200, 1, 1, None) == INV
 

@@ -46,24 +46,38 @@ __device__ __forceinline__ void put_four_once(const Int8Args &a, int64_t m, int6
     __builtin_nontemporal_store(__builtin_bit_cast(u32x4, v), (u32x4_any *)(a.C + at * 4));
 }
 
-// From the sums of four neighbouring outputs n .. n + 3 of row m to C, one after the other.
-__device__ __forceinline__ void finish_four(const Int8Args &a, int64_t m, int64_t n, f32x4 sum) {
-  const float sa = a.sa[m];
-  const f32x4 sb = vector_four(a, a.sb, n);
-  f32x4 v = {0, 0, 0, 0};
-  if (a.bias) v = vector_four(a, a.bias, n);
-#pragma unroll
-  for (int i = 0; i < 4; ++i) v[i] = scaled(sum[i], sa, sb[i], v[i]);
+// What four neighbouring outputs n .. n + 3 of row m take besides their sums.
+struct Extras {
+  float sa;
+  f32x4 sb, bias, source;
+};
+__device__ __forceinline__ Extras extras_of(const Int8Args &a, int64_t m, int64_t n) {
+  Extras x{a.sa[m], vector_four(a, a.sb, n), {0, 0, 0, 0}, {0, 0, 0, 0}};
+  if (a.bias) x.bias = vector_four(a, a.bias, n);
   if (a.source) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       if (n + i >= a.N) break;
       const int64_t at = m * a.N + n + i;
-      v[i] += a.src_bf16 ? __uint_as_float((uint32_t)((const uint16_t *)a.source)[at] << 16)
-                         : ((const float *)a.source)[at];
+      x.source[i] = a.src_bf16 ? __uint_as_float((uint32_t)((const uint16_t *)a.source)[at] << 16)
+                               : ((const float *)a.source)[at];
     }
   }
+  return x;
+}
+// From their sums to C.
+__device__ __forceinline__ void finish_four(const Int8Args &a, int64_t m, int64_t n, const f32x4 &sum,
+                                            const Extras &x) {
+  f32x4 v;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    v[i] = scaled(sum[i], x.sa, x.sb[i], x.bias[i]);
+    if (a.source) v[i] += x.source[i];
+  }
   put_four(a, m, n, v);
+}
+__device__ __forceinline__ void finish_four(const Int8Args &a, int64_t m, int64_t n, const f32x4 &sum) {
+  finish_four(a, m, n, sum, extras_of(a, m, n));
 }
 
 // Sums stay in int32 up to this many blocks of 128 along K (128^2 K < 2^31); past it K is cut.

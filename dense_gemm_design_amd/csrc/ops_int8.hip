@@ -25,8 +25,8 @@ __device__ __forceinline__ f32x4 floats(const i32x4 &v) {
 
 // Up to 16 FM rows of A: what counts is to read B once at the memory's rate.  A workgroup takes 16 rows
 // of B (columns of C); its eight waves take every eighth k-block (of its piece of K) straight into
-// registers, and their sums meet in LDS.  1 x 4096 x 4096 takes 5.9 us (7.4 with 32 columns a workgroup), 1 x
-// 16384 x 16384 54 us, 5.0 TB/s.
+// registers, and their sums meet in LDS.  1 x 4096 x 4096 takes 5.5 us (5.9 with the scales loaded
+// last, 7.4 with 32 columns a workgroup), 1 x 16384 x 16384 54 us, 5.0 TB/s.
 template <int FM>
 __global__ void __launch_bounds__(512) few_kernel(const Int8Args a) {
   constexpr int WAVES = 8, AHEAD = 4;   // AHEAD: k-blocks of a wave whose loads are in flight together
@@ -39,6 +39,11 @@ __global__ void __launch_bounds__(512) few_kernel(const Int8Args a) {
   const auto rb = make_rsrc(a.B + n0 * a.ldb, rows_b * a.ldb);
   const int split = blockIdx.y;
   const int32_t kb1 = (int32_t)((int64_t)a.kb * (split + 1) / a.splits);
+  // the four columns of one row that a lane finishes; what they take besides the sums is loaded first
+  const int64_t m = threadIdx.x / 64 * 16 + lane / 4, n = n0 + lane % 4 * 4;
+  const bool mine = threadIdx.x < FM * 64 && m < a.M && n < a.N;
+  Extras extras;
+  if (mine && a.splits == 1) extras = extras_of(a, m, n);
   i32x4 acc[FM];
 #pragma unroll
   for (int f = 0; f < FM; ++f) acc[f] = i32x4{0, 0, 0, 0};
@@ -74,40 +79,44 @@ __global__ void __launch_bounds__(512) few_kernel(const Int8Args a) {
 #pragma unroll
     for (int e = 0; e < 4; ++e) part[wave][f][r16][g4 * 4 + e] = acc[f][e];
   __syncthreads();
-  for (int i = threadIdx.x; i < FM * 64; i += WAVES * 64) {
-    const int f = i / 64, m16 = i / 4 % 16, q = i % 4;
-    const int64_t m = f * 16 + m16, n = n0 + q * 4;
-    if (m >= a.M || n >= a.N) continue;
-    i32x4 v = {0, 0, 0, 0};
+  if (!mine) return;
+  const int f = threadIdx.x / 64, m16 = lane / 4, q = lane % 4;
+  i32x4 v = {0, 0, 0, 0};
 #pragma unroll
-    for (int w = 0; w < WAVES; ++w)
+  for (int w = 0; w < WAVES; ++w)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) v[e] += part[w][f][m16][q * 4 + e];
-    if (a.splits == 1) {
-      finish_four(a, m, n, floats(v));
-      continue;
-    }
-    int *const p = (int *)a.partials + ((int64_t)split * a.M + m) * a.N + n;
-    if (n + 4 <= a.N) {
-      *(i32x4_any *)p = v;
-    } else {
+    for (int e = 0; e < 4; ++e) v[e] += part[w][f][m16][q * 4 + e];
+  if (a.splits == 1) {
+    finish_four(a, m, n, floats(v), extras);
+    return;
+  }
+  int *const p = (int *)a.partials + ((int64_t)split * a.M + m) * a.N + n;
+  if (n + 4 <= a.N) {
+    *(i32x4_any *)p = v;
+  } else {
 #pragma unroll
-      for (int e = 0; e < 4; ++e)
-        if (n + e < a.N) p[e] = v[e];
-    }
+    for (int e = 0; e < 4; ++e)
+      if (n + e < a.N) p[e] = v[e];
   }
 }
 
-// The sums of `splits` pieces, `pitch` apart, in 64 bits; `n` of the four are there.
+// ---- pieces of K ------------------------------------------------------------------------------
+
+// Adds the `splits` pieces of four sums, `pitch` apart, in 64 bits; `n` of the four are there, none where it is
+// not positive.  PARTS lanes of the workgroup, 256 apart, take every PARTS-th piece each; the first has the
+// result.  One trip to other XCDs' results for eight pieces takes 2 to 3 us: 40 x 320 x 32896, 24 pieces, in one
+// part 16.0 us, in four 13.0.
+template <int PARTS>
 __device__ __forceinline__ f32x4 joined(const int *p, int64_t pitch, int splits, int64_t n) {
+  const int part = PARTS > 1 ? threadIdx.x >> 8 : 0;
   int64_t v[4] = {0, 0, 0, 0};
-  for (int s = 0; s < splits; s += 8) {
+  for (int s = part; s < splits; s += 8 * PARTS) {
     i32x4 q[8];   // loads in flight together
 #pragma unroll
     for (int u = 0; u < 8; ++u) {
       q[u] = i32x4{0, 0, 0, 0};
-      if (s + u >= splits) continue;
-      const int *const x = p + (s + u) * pitch;
+      if (s + u * PARTS >= splits) continue;
+      const int *const x = p + (s + u * PARTS) * pitch;
       if (n >= 4) {
         q[u] = *(const i32x4_any *)x;
       } else {
@@ -121,16 +130,38 @@ __device__ __forceinline__ f32x4 joined(const int *p, int64_t pitch, int splits,
 #pragma unroll
       for (int e = 0; e < 4; ++e) v[e] += q[u][e];
   }
+  if constexpr (PARTS > 1) {
+    __shared__ int64_t more[PARTS - 1][4][256];
+    const int at = threadIdx.x & 255;
+    __syncthreads();   // those of the round before are read
+    if (part > 0) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) more[part - 1][e][at] = v[e];
+    }
+    __syncthreads();
+    if (part == 0) {
+#pragma unroll
+      for (int k = 0; k < PARTS - 1; ++k)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[e] += more[k][e][at];
+    }
+  }
   return f32x4{(float)v[0], (float)v[1], (float)v[2], (float)v[3]};
 }
+constexpr int kPartsFrom = 9;   // pieces from which on four parts add them
 
 // Adds the pieces of few rows, then the epilogue.
-__global__ void __launch_bounds__(256) join_kernel(const Int8Args a) {
+template <int PARTS>
+__global__ void __launch_bounds__(256 * PARTS) join_kernel(const Int8Args a) {
   const int64_t per_row = (a.N + 3) / 4, all = a.M * per_row;
-  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < all; i += (int64_t)gridDim.x * 256) {
-    const int64_t m = i / per_row, n = i % per_row * 4;
-    finish_four(a, m, n,
-                joined((const int *)a.partials + m * a.N + n, a.M * a.N, a.splits, a.N - n));
+  for (int64_t i0 = (int64_t)blockIdx.x * 256; i0 < all; i0 += (int64_t)gridDim.x * 256) {
+    const int64_t i = i0 + (threadIdx.x & 255);
+    const bool there = i < all;
+    const int64_t m = there ? i / per_row : 0, n = there ? i % per_row * 4 : 0;
+    const Extras x = extras_of(a, m, n);
+    const f32x4 sum = joined<PARTS>((const int *)a.partials + m * a.N + n, a.M * a.N, a.splits,
+                                    there ? a.N - n : 0);
+    if (there && threadIdx.x < 256) finish_four(a, m, n, sum, x);
   }
 }
 
@@ -150,11 +181,28 @@ __device__ __forceinline__ int32_t place(int32_t i, int32_t n) {
   return x * per + (x < more ? x : more) + i / 8;
 }
 
-// Writes a lane's FM x FN quads of sums, quad (f, g) at row ml0 + 16 f and column nl0 + 16 g of the tile at
-// (m0, n0): as they are to its piece of the partial sums, or finished to C.
+// Scales and bias of a lane's FM x FN quads, quad (f, g) at row m + 16 f and column n + 16 g.
+template <int FM, int FN>
+struct Scales {
+  f32x4 bias[FN], sb[FN];
+  float sa[FM];
+  __device__ __forceinline__ void load(const Int8Args &a, int64_t m, int64_t n) {
+    if (a.N < 4) return;
+#pragma unroll
+    for (int g = 0; g < FN; ++g) {
+      bias[g] = bias_four(a, n + g * 16);
+      sb[g] = vector_four(a, a.sb, n + g * 16);
+    }
+#pragma unroll
+    for (int f = 0; f < FM; ++f) sa[f] = a.sa[m + f * 16 < a.M ? m + f * 16 : a.M - 1];
+  }
+};
+
+// Writes a lane's quads of sums, at row ml0 + 16 f and column nl0 + 16 g of the tile at (m0, n0): as they are
+// to its piece of the partial sums, or finished to C.
 template <int BM, int BN, int FM, int FN, class Get>
 __device__ __forceinline__ void write_blocks(const Int8Args &a, int32_t piece, int64_t m0, int64_t n0,
-                                             int ml0, int nl0, Get get) {
+                                             int ml0, int nl0, const Scales<FM, FN> &x, Get get) {
   if (piece >= 0 || a.N < 4) {
 #pragma unroll
     for (int f = 0; f < FM; ++f) {
@@ -171,18 +219,6 @@ __device__ __forceinline__ void write_blocks(const Int8Args &a, int32_t piece, i
       }
     }
     return;
-  }
-  f32x4 bias[FN], sb[FN];
-#pragma unroll
-  for (int g = 0; g < FN; ++g) {
-    bias[g] = bias_four(a, n0 + nl0 + g * 16);
-    sb[g] = vector_four(a, a.sb, n0 + nl0 + g * 16);
-  }
-  float sa[FM];
-#pragma unroll
-  for (int f = 0; f < FM; ++f) {
-    const int64_t m = m0 + ml0 + f * 16;
-    sa[f] = a.sa[m < a.M ? m : a.M - 1];
   }
   with_source(a, [&](auto src_c) {
     constexpr int SRC = decltype(src_c)::value, STEP = FM < 2 ? 1 : 2;
@@ -204,7 +240,7 @@ __device__ __forceinline__ void write_blocks(const Int8Args &a, int32_t piece, i
           f32x4 v = floats(get(f0 + f, g));
           if (m >= a.M || n >= a.N) continue;
 #pragma unroll
-          for (int e = 0; e < 4; ++e) v[e] = scaled(v[e], sa[f0 + f], sb[g][e], bias[g][e]);
+          for (int e = 0; e < 4; ++e) v[e] = scaled(v[e], x.sa[f0 + f], x.sb[g][e], x.bias[g][e]);
           if constexpr (SRC != SRC_NONE) v += source_four<SRC>(a, n, src[f][g]);
           put_four(a, m, n, v);
         }
@@ -299,6 +335,13 @@ __global__ void __launch_bounds__(KG *WGM *WGN * 64) tile_kernel(const Int8Args 
   // a wave wholly past the edge only loads
   const bool inside = m0 + wm * WM < a.M && n0 + wn * WN < a.N;
 
+  // what the end takes besides the sums, ahead of everything: 188 x 108 x 1316 5.5 us, 5.8 with it
+  // at the end; 64 x 14336 x 4096 12.8, 13.2
+  constexpr int OWN = FM / KG;
+  const int ml0 = wm * WM + group * OWN * 16 + r16, nl0 = wn * WN + g4 * 4;
+  Scales<OWN, FN> scales;
+  if (piece < 0) scales.load(a, m0 + ml0, n0 + nl0);
+
 #pragma unroll
   for (int j = 0; j < AHEAD; ++j) load_next();
   int s = group;
@@ -327,7 +370,7 @@ __global__ void __launch_bounds__(KG *WGM *WGN * 64) tile_kernel(const Int8Args 
   asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
 
   // each group gives away the sums of the rows of blocks that the other one writes
-  constexpr int OWN = FM / KG, HALF = NW * OWN * FN * 1024;
+  constexpr int HALF = NW * OWN * FN * 1024;
   static_assert(KG == 1 || (KG == 2 && OWN * KG == FM && 2 * HALF <= S * STAGE), "");
   if constexpr (KG == 2) {
     typedef i32x4 __attribute__((address_space(3))) *i4p;
@@ -346,8 +389,7 @@ __global__ void __launch_bounds__(KG *WGM *WGN * 64) tile_kernel(const Int8Args 
         acc[f][g] = (group ? acc[f + OWN][g] : acc[f][g]) +
                     *(i4p)(area + group * HALF + (f * FN + g) * 1024);
   }
-  const int ml0 = wm * WM + group * OWN * 16 + r16, nl0 = wn * WN + g4 * 4;
-  write_blocks<BM, BN, OWN, FN>(a, piece, m0, n0, ml0, nl0,
+  write_blocks<BM, BN, OWN, FN>(a, piece, m0, n0, ml0, nl0, scales,
                                 [&](int f, int g) { return acc[f][g]; });
 }
 
@@ -544,7 +586,9 @@ pipe_kernel(const Int8Args a) {
       stage = after(stage);
       read_first_half();
     }
-    write_blocks<BM, BN, FM, FN>(a, w.piece, w.m0, w.n0, wm * WM + r16, wn * WN + g4 * 4,
+    Scales<FM, FN> scales;
+    if (w.piece < 0) scales.load(a, w.m0 + wm * WM + r16, w.n0 + wn * WN + g4 * 4);
+    write_blocks<BM, BN, FM, FN>(a, w.piece, w.m0, w.n0, wm * WM + r16, wn * WN + g4 * 4, scales,
                                  [&](int f, int g) {
                                    return i32x4{acc_read(acc[f][g][0]), acc_read(acc[f][g][1]),
                                                 acc_read(acc[f][g][2]), acc_read(acc[f][g][3])};
@@ -554,18 +598,20 @@ pipe_kernel(const Int8Args a) {
 }
 
 // Adds the pieces of the tiles whose K is cut, then the epilogue.  1024 elements of a tile a workgroup.
-__global__ void __launch_bounds__(256) join_tiles_kernel(const Int8Args a) {
+template <int PARTS>
+__global__ void __launch_bounds__(256 * PARTS) join_tiles_kernel(const Int8Args a) {
   const int32_t size = a.bm * a.bn, quads = a.bn / 4, groups = size / 1024;
   const int32_t cut = a.mt * a.nt - a.whole, at = blockIdx.x / groups;
-  const int32_t i = blockIdx.x % groups * 256 + threadIdx.x;
+  const int32_t i = blockIdx.x % groups * 256 + (threadIdx.x & 255);
   const int32_t ml = i / quads, nl = i % quads * 4;
   int64_t m0, n0;
   tile_corner(a, a.whole + at, a.bm, a.bn, m0, n0);
-  const int64_t m = m0 + ml, n = n0 + nl;
-  if (m >= a.M || n >= a.N) return;
-  finish_four(a, m, n,
-              joined((const int *)a.partials + (int64_t)at * size + ml * a.bn + nl, (int64_t)cut * size,
-                     a.splits, 4));
+  const bool there = m0 + ml < a.M && n0 + nl < a.N;
+  const int64_t m = there ? m0 + ml : 0, n = there ? n0 + nl : 0;
+  const Extras x = extras_of(a, m, n);
+  const f32x4 sum = joined<PARTS>((const int *)a.partials + (int64_t)at * size + ml * a.bn + nl,
+                                  (int64_t)cut * size, a.splits, there ? 4 : 0);
+  if (there && threadIdx.x < 256) finish_four(a, m, n, sum, x);
 }
 
 // ---- choice -----------------------------------------------------------------------------------
@@ -834,13 +880,12 @@ extern "C" int gemm_int8_run(const gemm_int8_desc *d, const void *A, const float
   if (hipGetLastError() != hipSuccess) return GEMM_ERR_HIP;
   if (p.splits > 1) {
     const int64_t few = (d->M * ((d->N + 3) / 4) + 255) / 256;
-    if (p.tiles < 0)
-      hipLaunchKernelGGL(join_kernel, dim3((uint32_t)(few < 8 * kCUs ? few : 8 * kCUs)), dim3(256), 0, s,
-                         a);
-    else
-      hipLaunchKernelGGL(join_tiles_kernel,
-                         dim3((uint32_t)((p.mt * p.nt - p.whole) * (a.bm * a.bn / 1024))), dim3(256), 0, s,
-                         a);
+    const bool parts = p.splits >= kPartsFrom;
+    const auto join = p.tiles < 0 ? (parts ? join_kernel<4> : join_kernel<1>)
+                                  : (parts ? join_tiles_kernel<4> : join_tiles_kernel<1>);
+    const int64_t groups = p.tiles < 0 ? (few < 8 * kCUs ? few : 8 * kCUs)
+                                       : (int64_t)(p.mt * p.nt - p.whole) * (a.bm * a.bn / 1024);
+    hipLaunchKernelGGL(join, dim3((uint32_t)groups), dim3(parts ? 1024 : 256), 0, s, a);
     if (hipGetLastError() != hipSuccess) return GEMM_ERR_HIP;
   }
   return GEMM_OK;

@@ -513,6 +513,13 @@ int check(int64_t rows, int64_t cols, bool rows_side, bool cols_side) {
   return GEMM_OK;
 }
 
+struct Span {
+  uintptr_t first, last;
+};
+Span span(const void *p, uintptr_t bytes) {
+  return p ? Span{(uintptr_t)p, (uintptr_t)p + bytes} : Span{0, 0};
+}
+
 bool aligned(const void *p, uintptr_t n) { return ((uintptr_t)p & (n - 1)) == 0; }
 
 }  // namespace
@@ -551,6 +558,19 @@ extern "C" int gemm_int8_quantize(const void *x, int dtype, int64_t rows, int64_
   if (!aligned(x, dtype == GEMM_BF16 ? 2 : 4) || !aligned(codes, 16) || !aligned(codes_t, 16) ||
       !aligned(scales, 4) || !aligned(scales_t, 4) || !aligned(workspace, 4))
     return GEMM_ERR_ALIGNMENT;
+  // workgroups read x again after others have written: nothing of what is written may overlap anything else
+  const uintptr_t es = dtype == GEMM_BF16 ? 2 : 4;
+  const Span spans[] = {
+      span(x, ((uintptr_t)(rows - 1) * (uintptr_t)stride + (uintptr_t)cols) * es),
+      span(codes, (uintptr_t)rows * (uintptr_t)pitch),
+      span(codes ? scales : nullptr, (uintptr_t)rows * 4),
+      span(codes_t, (uintptr_t)cols * (uintptr_t)pitch_t),
+      span(codes_t ? scales_t : nullptr, (uintptr_t)cols * 4),
+      span(workspace, need),
+  };
+  for (int i = 0; i < 6; ++i)
+    for (int j = i + 1; j < 6; ++j)
+      if (spans[i].first < spans[j].last && spans[j].first < spans[i].last) return GEMM_ERR_INVALID_ARG;
   RowQuantArgs a{};
   a.x = x;
   a.rows = rows;

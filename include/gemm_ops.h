@@ -120,7 +120,8 @@ int gemm_clip_grad_norm(const gemm_tensor *list, int64_t count, float max_norm, 
  *   -127 and 127; NaN and zeros for a row that holds an infinity or a NaN.
  * codes: rows x pitch bytes, pitch = cols rounded up to 16, zeros behind each row's codes; scales: one a
  * row.  codes_t, scales_t: the same of x transposed (cols x rows).  Either side may be NULL.  codes and
- * codes_t are 16-byte aligned. */
+ * codes_t are 16-byte aligned.  Where something that is written overlaps x or anything else:
+ * GEMM_ERR_INVALID_ARG. */
 int gemm_int8_quantize_workspace(int64_t rows, int64_t cols, int rows_side, int cols_side,
                                  size_t *bytes);
 int gemm_int8_quantize(const void *x, int dtype, int64_t rows, int64_t cols, int64_t stride,

@@ -140,6 +140,18 @@ def test_c_abi_refusals():
                      (dict(rows=1 << 31, cols=1 << 31, stride=1 << 31), UNS),
                      (dict(rows=1 << 23, codes_t=None, pitch=208), UNS)):
         assert quant(**kw) == want, kw
+    # 30 x 200 fp32 at P, and what is written, each at a place of its own or on another's last bytes
+    apart = dict(codes=P + (1 << 16), scales=P + (2 << 16), codes_t=P + (3 << 16), scales_t=P + (4 << 16),
+                 ws=P + (5 << 16))
+    if not torch.cuda.is_available():
+        assert quant(**apart) == L.GEMM_ERR_HIP
+    for kw in (dict(codes=P + 29 * 800 + 784), dict(codes=P - 30 * 208 + 16), dict(scales=P + 23996),
+               dict(codes_t=P + 23984), dict(scales_t=P - 796), dict(codes_t=P + (1 << 16) + 29 * 208),
+               dict(scales=P + (3 << 16) + 6396), dict(scales_t=P + (2 << 16) + 116)):
+        assert quant(**{**apart, **kw}) == INV, kw
+    assert quant(rows=3000, pitch_t=3008, **{**apart, "codes": P + (1 << 26), "ws": P + 30}) == ALI
+    far = dict(codes=P + (1 << 26), scales=P + (2 << 26), codes_t=P + (3 << 26), scales_t=P + (4 << 26))
+    assert quant(rows=3000, pitch_t=3008, ws=P + 2399996, **far) == INV   # x and the workspace
     n = ctypes.c_size_t()
     assert lib.gemm_int8_quantize_workspace(30, 200, 1, 0, ctypes.byref(n)) == 0 and n.value == 0
     assert lib.gemm_int8_quantize_workspace(3000, 200, 1, 1, ctypes.byref(n)) == 0 and n.value > 0

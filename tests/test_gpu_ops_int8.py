@@ -202,7 +202,14 @@ def test_product_large(dev, M, N, K, out):
     a, b = operand(g, M, K, dev), operand(g, N, K, dev)
     bias = randn(g, N).to(dev)
     check_product(a, b, out, "bias", bias=bias)
-    check_product(a, b, out, "source", source=randn(g, M, N).to(dev))
+    src = randn(g, M, N).to(dev)
+    got = check_product(a, b, out, "source", source=src)
+    if out == F32:   # the source itself
+        assert torch.equal(dg.int8_gemm(a, b, source=src, out=src), got)
+    else:
+        src = src.to(BF16)
+        got = check_product(a, b, out, "bf16 source", bias=bias, source=src)
+        assert torch.equal(dg.int8_gemm(a, b, bias_col=bias, source=src, out=src), got)
 
 
 @pytest.mark.parametrize("M,N,K", [(3, 20, 131071), (3, 20, 131072), (40, 70, 262145), (130, 140, 140000),

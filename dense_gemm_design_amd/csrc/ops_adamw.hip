@@ -61,6 +61,7 @@ struct Step {
   double beta1, beta2;          // for what step_at and lr_at say
   float b1, b1_rest, b2, b2_rest, eps, decay, max_norm;
   float lr, rate, root;         // rate = lr / (1 - b1^t), root = 1 / sqrt(1 - b2^t)
+  float up;                     // a power of two for both sides of the quotient (eps has it already)
 };
 static_assert(sizeof(Table<false>) + sizeof(Step) + 16 <= 4096, "kernel arguments");
 static_assert(sizeof(Table<true>) + sizeof(Step) + 16 <= 4096, "kernel arguments");
@@ -302,6 +303,8 @@ __global__ void __launch_bounds__(kThreads) adamw_kernel(const Table<COPIES> t, 
       now.rate = lr * a.rate;   // of a rate of one
     }
   }
+  now.rate *= a.up;
+  now.root *= a.up;
   if (a.norm) {
     now.c = a.max_norm / (*a.norm + 1e-6f);
     if (now.c > 1.0f) now.c = 1.0f;   // a NaN stays
@@ -461,7 +464,11 @@ extern "C" int gemm_adamw_step(const gemm_adamw_tensor *list, int64_t count,
   a.b1_rest = (float)(1.0 - d->beta1);
   a.b2 = (float)d->beta2;
   a.b2_rest = (float)(1.0 - d->beta2);
-  a.eps = (float)d->eps;
+  // The reciprocal's instruction takes a number under 2^-126 for zero, and a moment of zero over that would be
+  // NaN: where eps may be one, both sides of the quotient are 2^24 times as large, eps 2^-149 at least.
+  const bool tiny = d->eps > 0.0 && d->eps < 0x1p-100;
+  a.up = tiny ? 0x1p24f : 1.0f;
+  a.eps = tiny ? fmaxf((float)(d->eps * 0x1p24), 0x1p-125f) : (float)d->eps;
   a.decay = (float)d->weight_decay;
   a.max_norm = (float)d->max_norm;
   a.lr = (float)d->lr;

@@ -176,7 +176,7 @@ typedef struct {
 
 /* m = beta1 m + (1 - beta1) g, v = beta2 v + (1 - beta2) g^2, and
  * param -= lr (weight_decay param + (m / (1 - beta1^step)) / (sqrt(v / (1 - beta2^step)) + eps)),
- * in fp32, rounded once.  e4m3 states are rounded to nearest behind that: codes of x / s with
+ * in fp32, rounded once (an eps that is not zero counts as 2^-149 at least).  e4m3 states are rounded to nearest behind that: codes of x / s with
  * s = max(amax / 448, 2^-126) of each 128 (NaN where they hold an infinity or a NaN), a root that is not
  * zero never to zero.  Where something that is written overlaps anything else (a parameter that is in the
  * list twice): GEMM_ERR_INVALID_ARG. */

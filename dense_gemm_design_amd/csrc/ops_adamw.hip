@@ -130,7 +130,9 @@ __device__ __forceinline__ u32x2_t encode8(const float (&x)[8], float *s) {
 #pragma unroll
   for (int i = 0; i < 8; ++i) top = max(top, bits_of(x[i]) & 0x7FFFFFFFu);
   const float amax = row16_amax(float_of(top));
-  float scale = fmaxf(amax * (1.0f / 448.0f), 0x1p-126f);
+  // the quotient rounded to nearest: one step of correction makes amax * (1 / 448) exact
+  const float y = 1.0f / 448.0f, near = amax * y;
+  float scale = fmaxf(fmaf(fmaf(-448.0f, near, amax), y, near), 0x1p-126f);
   if (!(amax < __builtin_inff())) scale = float_of(0x7FC00000u);
   *s = scale;
   const float r = scale == scale ? __builtin_amdgcn_rcpf(scale) : scale;

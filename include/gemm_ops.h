@@ -176,10 +176,11 @@ typedef struct {
 
 /* m = beta1 m + (1 - beta1) g, v = beta2 v + (1 - beta2) g^2, and
  * param -= lr (weight_decay param + (m / (1 - beta1^step)) / (sqrt(v / (1 - beta2^step)) + eps)),
- * in fp32, rounded once (an eps that is not zero counts as 2^-149 at least).  e4m3 states are rounded to nearest behind that: codes of x / s with
- * s = max(amax / 448, 2^-126) of each 128 (NaN where they hold an infinity or a NaN), a root that is not
- * zero never to zero.  Where something that is written overlaps anything else (a parameter that is in the
- * list twice): GEMM_ERR_INVALID_ARG. */
+ * in fp32, rounded once (an eps that is not zero counts as 2^-149 at least).  e4m3 states are rounded behind
+ * that: s = max(amax / 448, 2^-126) of each 128, the quotient rounded to nearest (NaN where they hold an
+ * infinity or a NaN), and codes of x (1 / s) in fp32, to nearest, so that an x / s within 2^-22 of a border
+ * between two codes may go to either; a root that is not zero never to zero.  Where something that is
+ * written overlaps anything else (a parameter that is in the list twice): GEMM_ERR_INVALID_ARG. */
 int gemm_adamw_step(const gemm_adamw_tensor *list, int64_t count, const gemm_adamw_desc *desc,
                     void *stream);
 

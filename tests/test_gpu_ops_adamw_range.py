@@ -32,3 +32,17 @@ def test_eps_of_any_size(dev, eps, state):
         s = dg.adamw_state(params, state)
         s.m[:700] = max(eps * 1e4, 2.0 ** -125)
         step_and_check(params, [torch.zeros(700, device=dev)], s, 3, f"eps {eps} alone", eps=eps)
+
+
+def test_scales_are_the_rounded_quotient(dev):
+    """Where moments are the gradients (no memory), a block's scale is amax / 448 rounded to nearest.  (The
+    exact quotient is no fp32 midpoint, and further from one than fp64's places: it is one of sevenths.)"""
+    g = gen(21)
+    n = 4000 * 128
+    x = randn(g, n) * torch.exp(randn(g, 4000) * 8).repeat_interleave(128)
+    p = torch.zeros(n, device=dev)
+    s = dg.adamw_state([p], "e4m3")
+    dg.adamw_step([p], [x.to(dev)], s, 1, 1e-3, betas=(0.0, 0.0))
+    want = (x.view(-1, 128).abs().amax(1).double() / 448).float()
+    assert float(want.min()) > 2.0 ** -126
+    assert torch.equal(s.m_scales.cpu(), want)

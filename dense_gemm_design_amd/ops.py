@@ -11,6 +11,7 @@ carry no history, whether or not the arguments require gradients, so a backward 
 (csrc/binding.cpp); load() gives the C ABI itself through ctypes.
 """
 import ctypes
+import warnings
 
 from . import _lib
 
@@ -261,6 +262,8 @@ def clip_grad_norm(grads, max_norm, out=None):
 
 # ---- AdamW ------------------------------------------------------------------------------------
 
+_MOST_BETA2 = 0.95   # that e4m3 states follow
+
 class AdamWState:
     """The moments of a list of parameters, one after the other, each parameter's from a multiple of
     128 elements on.
@@ -289,7 +292,7 @@ class AdamWState:
 
 def adamw_state(params, dtype="e4m3"):
     """The state of a list of parameters on one GPU before their first step: zeros.  dtype: "f32", 8 bytes
-    a parameter, or "e4m3", 2.06."""
+    a parameter, or "e4m3", 2.06, for a beta2 of at most 0.95 (see adamw_step)."""
     import torch
     if dtype not in ("e4m3", "f32"):
         raise ValueError(f'dtype must be "e4m3" or "f32"; got {dtype!r}')
@@ -305,13 +308,20 @@ def adamw_state(params, dtype="e4m3"):
     return AdamWState(*codes, *scales)
 
 
-def adamw_step(params, grads, state, step, lr, betas=(0.9, 0.999), eps=1e-8, weight_decay=0.01,
+def adamw_step(params, grads, state, step, lr, betas=None, eps=1e-8, weight_decay=0.01,
                norm=None, max_norm=None, copies=None):
     """Steps a list of parameters (float32 or bfloat16, packed, on one GPU) and its state in place:
     m = beta1 m + (1 - beta1) g, v = beta2 v + (1 - beta2) g^2, and each parameter loses
     lr (weight_decay parameter + (m / (1 - beta1^step)) / (sqrt(v / (1 - beta2^step)) + eps)), in float32,
     rounded once.  An e4m3 state is rounded to nearest behind that, a root of v that is not zero never to
-    zero; an infinity or a NaN in a gradient makes NaNs of the 128 moments around it.
+    zero; an infinity or a NaN in a gradient, or a square of one over float32's range, makes NaNs of the 128
+    moments around it.
+
+    betas: (0.9, 0.999), and (0.9, 0.95) for an e4m3 state.  Rounding to nearest holds no change of less than
+    half a code, 3 to 6 %, so under a beta2 near one a root does not come down after its gradients: where they
+    fall to a tenth beside larger ones of their block, it stays 1.02 times as large as it should be for a beta2
+    of 0.95, 7 times for 0.98, 11 times for 0.99, and the parameters move that much too slowly.  Over 0.95 a
+    warning says so; "f32" states hold any beta2.
 
     grads: one float32 or bfloat16 tensor a parameter.  state: of adamw_state(), for the same list.  step:
     this step's number, from 1, or an int64 tensor of one element; lr: a number, or a float32 tensor of
@@ -320,6 +330,10 @@ def adamw_step(params, grads, state, step, lr, betas=(0.9, 0.999), eps=1e-8, wei
     copies: bfloat16 tensors that the stepped parameters are also written to, or None for some or all."""
     if not isinstance(state, AdamWState):
         raise ValueError("state must be an AdamWState")
-    beta1, beta2 = betas
+    e4m3 = state.m_scales is not None
+    beta1, beta2 = ((0.9, _MOST_BETA2) if e4m3 else (0.9, 0.999)) if betas is None else betas
+    if e4m3 and float(beta2) > _MOST_BETA2:
+        warnings.warn(f"an e4m3 state does not follow second moments that fall under a beta2 of {beta2}, only up "
+                      f'to {_MOST_BETA2}; adamw_state(params, "f32") does', stacklevel=2)
     _binding().adamw_step(params, grads, state.m, state.v, state.m_scales, state.v_scales, step, lr,
                           beta1, beta2, eps, weight_decay, norm, max_norm, copies)

@@ -179,8 +179,10 @@ typedef struct {
  * in fp32, rounded once (an eps that is not zero counts as 2^-149 at least).  e4m3 states are rounded behind
  * that: s = max(amax / 448, 2^-126) of each 128, the quotient rounded to nearest (NaN where they hold an
  * infinity or a NaN), and codes of x (1 / s) in fp32, to nearest, so that an x / s within 2^-22 of a border
- * between two codes may go to either; a root that is not zero never to zero.  Where something that is
- * written overlaps anything else (a parameter that is in the list twice): GEMM_ERR_INVALID_ARG. */
+ * between two codes may go to either; a root that is not zero never to zero.  A change of less than half
+ * a code is lost in that: e4m3 states follow second moments that fall for a beta2 of up to 0.95.  Where
+ * something that is written overlaps anything else (a parameter that is in the list twice):
+ * GEMM_ERR_INVALID_ARG. */
 int gemm_adamw_step(const gemm_adamw_tensor *list, int64_t count, const gemm_adamw_desc *desc,
                     void *stream);
 

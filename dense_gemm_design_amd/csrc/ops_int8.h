@@ -80,9 +80,6 @@ __device__ __forceinline__ void finish_four(const Int8Args &a, int64_t m, int64_
   finish_four(a, m, n, sum, extras_of(a, m, n));
 }
 
-// Sums stay in int32 up to this many blocks of 128 along K (128^2 K < 2^31); past it K is cut.
-constexpr int32_t kMostBlocks = 1023;
-
 // ---- streams of instructions laid out by hand --------------------------------------------------
 
 // The accumulators stay in accumulation registers, named as both source and destination: given the builtin, the

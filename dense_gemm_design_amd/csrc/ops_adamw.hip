@@ -8,14 +8,15 @@
 // codes with an fp32 scale s = max(amax / 448, 2^-126) per 128 neighbours, x ~ s q.  (The root spans half of
 // v's powers of two, and is what divides.  One that is not zero keeps the smallest code at least: a first
 // moment over a root that was rounded to zero would be as large as 1 / eps.)  Codes are those of
-// x * (1 / s), so a quotient within 2^-22 of a border may go to either neighbour.
+// x * (1 / s), so a quotient within 2^-22 of a border may go to either neighbour.  A change of less than half a
+// code is lost: roots follow gradients that fall for b2 up to 0.95.
 //
 // The list goes to the kernels as a table in their arguments, as in ops_clip.hip, cut into chunks that
 // workgroups take in turn.  A lane takes eight neighbours, so a scale's 128 are a DPP row of 16 lanes.
 //
 // Bound by memory: parameters and states read and written once, gradients read once.  Many short workgroups
-// come nearest to it (310 M bf16 parameters with e4m3 states, 2.6 GB, in chunks of 2048, 4096, 8192, 16384:
-// 511, 466, 469, 498 us, 5.65 TB/s at best; 160 M fp32 ones with fp32 states and copies, 3.8 GB, of 1024, 2048,
+// come nearest to it (260 M bf16 parameters with e4m3 states, 2.6 GB, in chunks of 2048, 4096, 8192, 16384:
+// 511, 466, 469, 498 us, 5.65 TB/s at best; 134 M fp32 ones with fp32 states and copies, 3.8 GB, of 1024, 2048,
 // 4096, 16384: 640, 676, 733, 768 us, 5.9 TB/s; 2048 workgroups that stay: 556, 831), and loads and stores
 // past the caches (583 and 860 without).
 #include "../../include/gemm_ops.h"

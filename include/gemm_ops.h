@@ -121,7 +121,8 @@ int gemm_clip_grad_norm(const gemm_tensor *list, int64_t count, float max_norm, 
  * codes: rows x pitch bytes, pitch = cols rounded up to 16, zeros behind each row's codes; scales: one a
  * row.  codes_t, scales_t: the same of x transposed (cols x rows).  Either side may be NULL.  codes and
  * codes_t are 16-byte aligned.  Where something that is written overlaps x or anything else:
- * GEMM_ERR_INVALID_ARG. */
+ * GEMM_ERR_INVALID_ARG; where x has more than 2^24 - 1 blocks of 128 x 128, or rows alone are asked for of more
+ * than 4194303 of them: GEMM_ERR_UNSUPPORTED. */
 int gemm_int8_quantize_workspace(int64_t rows, int64_t cols, int rows_side, int cols_side,
                                  size_t *bytes);
 int gemm_int8_quantize(const void *x, int dtype, int64_t rows, int64_t cols, int64_t stride,
@@ -132,7 +133,8 @@ int gemm_int8_quantize(const void *x, int dtype, int64_t rows, int64_t cols, int
  *   scale_a[m] scale_b[n] * (sum over k of a b) + bias[n] + source[m, n].
  * The sum is exact; it is rounded to fp32, and so is what follows, C once more to its type.  An element
  * does not depend on the other rows and columns.  Scales are numbers of any size, or NaN; no step leaves
- * fp32's range where the scaled sum is in it.  N at most 2^22, lda and ldb 2^22. */
+ * fp32's range where the scaled sum is in it.  GEMM_ERR_UNSUPPORTED where N, lda or ldb is over 2^22, M over
+ * 2^31, or C has more than 2^22 tiles of 64 x 64, 2^19 where K is over 130944 and its sums come in pieces. */
 typedef struct {
   int64_t M, N, K;
   int64_t lda, ldb;            /* bytes from row to row: >= K, multiples of 16, zeros behind K  */
@@ -143,7 +145,7 @@ typedef struct {
 int gemm_int8_workspace(const gemm_int8_desc *desc, size_t *bytes);
 
 /* A, B 16-byte aligned; bias (N floats) and source (M x N, packed rows) or NULL.  The source may be C itself
- * if it has C's type; where it, the bias or a scale overlaps C otherwise: GEMM_ERR_INVALID_ARG. */
+ * if it has C's type; where it, the bias, a scale or an operand overlaps C otherwise: GEMM_ERR_INVALID_ARG. */
 int gemm_int8_run(const gemm_int8_desc *desc, const void *A, const float *scale_a, const void *B,
                   const float *scale_b, void *C, const float *bias, const void *source,
                   void *workspace, size_t workspace_bytes, void *stream);

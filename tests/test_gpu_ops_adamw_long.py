@@ -15,6 +15,13 @@ LR, BETAS, EPS, DECAY = 3e-3, (0.9, 0.95), 1e-8, 0.1
 PASSING, CHUNKS = 96 << 20, 4096 * 2048   # bytes and elements from which on the kernels go over
 
 
+@pytest.fixture(scope="module", autouse=True)
+def large_tensors_go_back():
+    """What torch keeps of them for other tests' tensors would count as memory in use there."""
+    yield
+    torch.cuda.empty_cache()
+
+
 def bytes_of(params, grads, copies, state):
     return sum(p.numel() * (2 * p.element_size() + g.element_size() + (4 if state == "e4m3" else 16)
                             + (2 if c is not None else 0)) for p, g, c in zip(params, grads, copies))

@@ -16,6 +16,13 @@ TYPES, NAMES = [BF16, F32], ["bf16", "f32"]
 U = R.U
 
 
+@pytest.fixture(scope="module", autouse=True)
+def large_tensors_go_back():
+    """What torch keeps of them for other tests' tensors would count as memory in use there."""
+    yield
+    torch.cuda.empty_cache()
+
+
 def operand(g, dev, rows, K, start):
     """Random codes between others: rows of `pitch`, from `start` bytes behind a line on where they may."""
     width, step = R.up(K, 16) * 16, pitch(K, start)
